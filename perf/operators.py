@@ -399,7 +399,7 @@ def _plan(s):
     offsets = torch.cat((ends.new_zeros(1), ends))
     old = (lens + ps - 1) // ps
     need = (lens + new + ps - 1) // ps - old
-    fits = (lens + new <= max_pages * ps) & (ends <= n)
+    fits = (lens + new <= max_pages * ps) & ((new == 0) | (ends <= n))
     need = torch.where(fits, need, torch.zeros_like(need))
     upto = torch.cumsum(need, 0)
     count = s["count"].long()

@@ -24,6 +24,8 @@ DA_ERR_WORKSPACE = -4
 DA_ERR_CUDA = -5
 DA_ERR_DEVICE_TIMEOUT = -6
 DA_ERR_SCHEDULE = -7
+DA_ERR_PAGE = -8
+DA_ERR_CACHE_FULL = -9
 DA_BF16 = 0
 DA_FP32 = 1
 
@@ -58,6 +60,18 @@ EXPORTS = (
     "diffattn_v2_bwd_saved",
     "diffattn_v2_prefill_oproj_workspace_size",
     "diffattn_v2_prefill_oproj",
+    "diffattn_page_plan",
+    "diffattn_page_release",
+    "diffattn_kv4_page_bytes",
+    "diffattn_kv4_append",
+    "diffattn_kv4_read",
+    "diffattn_v2_decode_kv4_workspace_size",
+    "diffattn_v2_decode_kv4",
+    "diffattn_v1_decode_kv4_workspace_size",
+    "diffattn_v1_decode_kv4",
+    "diffattn_qk_norm_rope",
+    "diffattn_qk_norm_rope_bwd_workspace_size",
+    "diffattn_qk_norm_rope_bwd",
     "diffattn_reset_tile_counters",
     "diffattn_selftest_hold_tile_counter",
     "diffattn_selftest_keep_tile_counter",
@@ -76,6 +90,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
@@ -162,6 +177,36 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.diffattn_v2_prefill_oproj.restype = _i
     lib.diffattn_v2_prefill_oproj.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                                               _i, _i, _i, _i, _vp, _sz, _vp, _vp]
+    lib.diffattn_page_plan.restype = _i
+    lib.diffattn_page_plan.argtypes = [_vp] * 5 + [_i] * 5 + [_vp] * 8
+    lib.diffattn_page_release.restype = _i
+    lib.diffattn_page_release.argtypes = [_vp] * 5 + [_i] * 4 + [_vp] * 2
+    lib.diffattn_kv4_page_bytes.restype = _sz
+    lib.diffattn_kv4_page_bytes.argtypes = [_i, _i, _i]
+    lib.diffattn_kv4_append.restype = _i
+    lib.diffattn_kv4_append.argtypes = [_vp, _ll, _vp, _ll, _i, _vp, _i, _i, _i, _vp, _i, _i, _vp,
+                                        _vp]
+    lib.diffattn_kv4_read.restype = _i
+    lib.diffattn_kv4_read.argtypes = [_vp, _i, _i, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp]
+    lib.diffattn_v2_decode_kv4_workspace_size.restype = _sz
+    lib.diffattn_v2_decode_kv4_workspace_size.argtypes = [_i, _i, _i]
+    lib.diffattn_v2_decode_kv4.restype = _i
+    lib.diffattn_v2_decode_kv4.argtypes = [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _i, _i,
+                                           _i, _i, _vp, _vp, _sz, _vp, _vp]
+    lib.diffattn_v1_decode_kv4_workspace_size.restype = _sz
+    lib.diffattn_v1_decode_kv4_workspace_size.argtypes = [_i, _i]
+    lib.diffattn_v1_decode_kv4.restype = _i
+    lib.diffattn_v1_decode_kv4.argtypes = [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _i, _i,
+                                           _i, _i, _vp, _i, _vp, _f, _f, _vp, _sz, _vp, _vp]
+    lib.diffattn_qk_norm_rope.restype = _i
+    lib.diffattn_qk_norm_rope.argtypes = [_vp, _ll, _vp, _ll, _i, _i, _i, _i, _i, _vp, _vp, _f,
+                                          _vp, _vp, _i, _i, _vp, _ll, _vp, _ll, _vp]
+    lib.diffattn_qk_norm_rope_bwd_workspace_size.restype = _sz
+    lib.diffattn_qk_norm_rope_bwd_workspace_size.argtypes = [_i, _i, _i, _i]
+    lib.diffattn_qk_norm_rope_bwd.restype = _i
+    lib.diffattn_qk_norm_rope_bwd.argtypes = [_vp, _ll, _vp, _ll, _i, _vp, _ll, _vp, _ll, _i, _i,
+                                              _i, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _vp, _vp,
+                                              _vp, _vp, _vp, _sz, _vp]
     lib.diffattn_reset_tile_counters.restype = _i
     lib.diffattn_reset_tile_counters.argtypes = [_vp]
     lib.diffattn_selftest_hold_tile_counter.restype = _i
@@ -600,6 +645,306 @@ def diffattn_selftest_wait_timeout(timeout_us, dev_status, waited_ns=None, strea
     _need_cuda(dev_status, waited_ns)
     _check("diffattn_selftest_wait_timeout", load().diffattn_selftest_wait_timeout(
         int(timeout_us), _ptr(dev_status), _ptr(waited_ns), _stream(stream)))
+
+
+# ---- serving: page plan, 4-bit paged cache, decode over it; QK norm + rotation
+class _On:
+    """The device of a call: checks that its tensors lie on it, makes it
+    current for the call, and gives the stream."""
+
+    def __init__(self, first, *others):
+        if not first.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        self.device = first.device
+        for t in others:
+            if t is not None and t.device != self.device:
+                raise ValueError("tensors lie on different devices (%s, %s)"
+                                 % (self.device, t.device))
+        self._guard = torch.cuda.device(self.device)
+
+    def __enter__(self):
+        self._guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _need(name, t, dtype, shape=None):
+    """A dense tensor of one type (and, entries of None aside, shape)."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and (t.dim() != len(shape) or any(
+            want is not None and want != have for want, have in zip(shape, t.shape))):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+
+
+def _token_stride(name, t, tokens=None, dtype=None):
+    """Token stride of t [T, H, d], whose heads of a token lie in a row."""
+    if t.dim() != 3 or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError("%s must be [tokens, heads, width], got %s" % (name, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    T, H, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError("%s: the heads of a token must lie in a row" % name)
+    return t.stride(0) if T > 1 else max(1, H) * d
+
+
+def _workspace(workspace, need, device, stream):
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        if stream is not None:   # freed on return: kept from reuse until that stream is past it
+            workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _kv4_cache(cache, n_kv_heads=None):
+    """(pages, KV heads, page size) of a cache [n_pages, n_kv_heads, page_size * 144]."""
+    _need("cache", cache, torch.uint8, (None, n_kv_heads, None))
+    if cache.shape[2] % 144:
+        raise ValueError("cache must be [n_pages, n_kv_heads, page_size * 144]")
+    return cache.shape[0], cache.shape[1], cache.shape[2] // 144
+
+
+def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count, page_size,
+                       n_slots, *, out=None, dev_status=None, stream=None):
+    """Pages, slots and positions of a step's new tokens.  new_lens,
+    cache_lens int32 [R]; block_table int32 [R, max_pages] (new pages written
+    in place); free_pages int32 [n_pages], a stack of which free_count int32
+    [1] are free.  Returns a dict: slots, positions [n_slots], offsets
+    [R + 1], served, cache_lens [R], free_count [1] (int32).  `out`, such a
+    dict, is written instead of new tensors; its cache_lens and free_count
+    may be the arguments themselves."""
+    i32 = torch.int32
+    R = new_lens.numel()
+    _need("new_lens", new_lens, i32, (R,))
+    _need("cache_lens", cache_lens, i32, (R,))
+    _need("block_table", block_table, i32, (R, None))
+    _need("free_pages", free_pages, i32, (None,))
+    _need("free_count", free_count, i32, (1,))
+    sizes = {"slots": n_slots, "positions": n_slots, "offsets": R + 1, "served": R,
+             "cache_lens": R, "free_count": 1}
+    if out is None:
+        # one allocation; the pieces start on 16-byte boundaries
+        at, total = {}, 0
+        for name, n in sizes.items():
+            at[name] = total
+            total += (n + 3) // 4 * 4
+        flat = torch.empty(total, dtype=i32, device=new_lens.device)
+        out = {name: flat[at[name]:at[name] + n] for name, n in sizes.items()}
+    for name, n in sizes.items():
+        _need(name, out[name], i32, (n,))
+    with _On(new_lens, cache_lens, block_table, free_pages, free_count, dev_status,
+             *out.values()):
+        _check("diffattn_page_plan", load().diffattn_page_plan(
+            _ptr(new_lens), _ptr(cache_lens), _ptr(block_table), _ptr(free_pages),
+            _ptr(free_count), R, block_table.shape[1], free_pages.numel(), int(page_size),
+            int(n_slots), _ptr(out["slots"]), _ptr(out["positions"]), _ptr(out["offsets"]),
+            _ptr(out["served"]), _ptr(out["cache_lens"]), _ptr(out["free_count"]),
+            _ptr(dev_status), _stream(stream)))
+    return out
+
+
+def diffattn_page_release(release, cache_lens, block_table, free_pages, free_count, page_size, *,
+                          dev_status=None, stream=None):
+    """Gives the pages of requests with release[r] != 0 back (int32 [R]);
+    cache_lens, block_table, free_pages and free_count are changed in place."""
+    i32 = torch.int32
+    R = release.numel()
+    _need("release", release, i32, (R,))
+    _need("cache_lens", cache_lens, i32, (R,))
+    _need("block_table", block_table, i32, (R, None))
+    _need("free_pages", free_pages, i32, (None,))
+    _need("free_count", free_count, i32, (1,))
+    with _On(release, cache_lens, block_table, free_pages, free_count, dev_status):
+        _check("diffattn_page_release", load().diffattn_page_release(
+            _ptr(release), _ptr(cache_lens), _ptr(block_table), _ptr(free_pages),
+            _ptr(free_count), R, block_table.shape[1], free_pages.numel(), int(page_size),
+            _ptr(dev_status), _stream(stream)))
+
+
+def diffattn_kv4_page_bytes(n_kv_heads, head_dim, page_size) -> int:
+    return int(load().diffattn_kv4_page_bytes(n_kv_heads, head_dim, page_size))
+
+
+def diffattn_kv4_append(k, v, slots, cache, *, dev_status=None, stream=None):
+    """Writes rows k, v [T, Hkv, 128] (bf16 or fp32; slices of a fused
+    projection are taken as they are) into the 4-bit cache
+    [n_pages, Hkv, page_size * 144] uint8 at slots int32 [T] (negative: skipped)."""
+    T, H, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v differ in shape")
+    ks, vs = _token_stride("k", k), _token_stride("v", v, T, k.dtype)
+    _need("slots", slots, torch.int32, (T,))
+    pages, _, ps = _kv4_cache(cache, H)
+    with _On(k, v, slots, cache, dev_status):
+        _check("diffattn_kv4_append", load().diffattn_kv4_append(
+            _ptr(k), ks, _ptr(v), vs, _dtype_code(k), _ptr(slots), T, H, d, _ptr(cache), pages,
+            ps, _ptr(dev_status), _stream(stream)))
+    return cache
+
+
+def diffattn_kv4_read(cache, slots, *, out=None, dtype=torch.bfloat16, dev_status=None,
+                      stream=None):
+    """Rows (k, v) [T, Hkv, 128] held at slots int32 [T].  Rows of negative
+    slots are left as they were in `out` = (k, v), or are 0 in new tensors."""
+    pages, H, ps = _kv4_cache(cache)
+    _need("slots", slots, torch.int32, (None,))
+    T = slots.shape[0]
+    if out is None:
+        out = tuple(torch.zeros(T, H, 128, dtype=dtype, device=cache.device) for _ in "kv")
+    k, v = out
+    _need("k", k, k.dtype, (T, H, 128))
+    _need("v", v, k.dtype, (T, H, 128))
+    with _On(cache, slots, k, v, dev_status):
+        _check("diffattn_kv4_read", load().diffattn_kv4_read(
+            _ptr(cache), pages, ps, _ptr(slots), T, H, 128, _ptr(k), _ptr(v), _dtype_code(k),
+            _ptr(dev_status), _stream(stream)))
+    return k, v
+
+
+def diffattn_v2_decode_kv4_workspace_size(batch, n_q_heads, n_kv_heads) -> int:
+    return int(load().diffattn_v2_decode_kv4_workspace_size(batch, n_q_heads, n_kv_heads))
+
+
+def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, workspace=None,
+                           out=None, dev_status=None, stream=None):
+    """V2 decode over the 4-bit cache.  q [B, Hq, 128] bf16; cache
+    [n_pages, Hkv, page_size * 144] uint8; block_table int32 [B, max_pages];
+    cache_lens int32 [B]; lam [Hq/2] fp32; out [B, Hq/2, 128]."""
+    dtype = _dtype_code(q)
+    B, Hq, d = q.shape
+    _need("q", q, q.dtype)
+    pages, Hkv, ps = _kv4_cache(cache)
+    _need("block_table", block_table, torch.int32, (B, None))
+    _need("cache_lens", cache_lens, torch.int32, (B,))
+    _need("lam", lam, torch.float32, (Hq // 2,))
+    if out is None:
+        out = torch.empty(B, Hq // 2, d, dtype=q.dtype, device=q.device)
+    _need("out", out, q.dtype, (B, Hq // 2, d))
+    with _On(q, cache, block_table, cache_lens, lam, workspace, out, dev_status) as on:
+        ws, ws_bytes = _workspace(workspace, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv),
+                                  on.device, stream)
+        _check("diffattn_v2_decode_kv4", load().diffattn_v2_decode_kv4(
+            _ptr(q), _ptr(cache), pages, ps, _ptr(block_table), block_table.shape[1],
+            _ptr(cache_lens), int(window), _ptr(out), dtype, B, Hq, Hkv, d, _ptr(lam), _ptr(ws),
+            ws_bytes, _ptr(dev_status), _stream(stream)))
+    return out
+
+
+def diffattn_v1_decode_kv4_workspace_size(batch, n_heads) -> int:
+    return int(load().diffattn_v1_decode_kv4_workspace_size(batch, n_heads))
+
+
+def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, apply_norm=False,
+                           norm_weight=None, norm_eps=1e-5, lambda_init=0.0, workspace=None,
+                           out=None, dev_status=None, stream=None):
+    """V1 decode over the 4-bit cache.  q [B, H, 128] bf16 (two 64-wide
+    branches); cache [n_pages, H, page_size * 144] uint8; out [B, H, 128]."""
+    dtype = _dtype_code(q)
+    B, H, d2 = q.shape
+    _need("q", q, q.dtype)
+    pages, _, ps = _kv4_cache(cache, H)
+    _need("block_table", block_table, torch.int32, (B, None))
+    _need("cache_lens", cache_lens, torch.int32, (B,))
+    _need("lam", lam, torch.float32, (H,))
+    if norm_weight is not None:
+        _need("norm_weight", norm_weight, torch.float32, (128,))
+    if out is None:
+        out = torch.empty(B, H, 128, dtype=q.dtype, device=q.device)
+    _need("out", out, q.dtype, (B, H, 128))
+    with _On(q, cache, block_table, cache_lens, lam, norm_weight, workspace, out,
+             dev_status) as on:
+        ws, ws_bytes = _workspace(workspace, diffattn_v1_decode_kv4_workspace_size(B, H),
+                                  on.device, stream)
+        _check("diffattn_v1_decode_kv4", load().diffattn_v1_decode_kv4(
+            _ptr(q), _ptr(cache), pages, ps, _ptr(block_table), block_table.shape[1],
+            _ptr(cache_lens), int(window), _ptr(out), dtype, B, H, d2 // 2, 128, _ptr(lam),
+            int(bool(apply_norm)), _ptr(norm_weight), float(norm_eps), float(lambda_init),
+            _ptr(ws), ws_bytes, _ptr(dev_status), _stream(stream)))
+    return out
+
+
+def _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight):
+    T, Hq, d = q.shape
+    qs = _token_stride("q", q)
+    Hk, ks = 0, 0
+    if k is not None:
+        ks = _token_stride("k", k, T, q.dtype)
+        Hk = k.shape[1]
+        if k.shape[2] != d:
+            raise ValueError("q and k differ in width")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(name, w, torch.float32, (d,))
+    rot = 0
+    if inv_freq is not None:
+        _need("inv_freq", inv_freq, torch.float32, (None,))
+        rot = 2 * inv_freq.shape[0]
+    if positions is not None:
+        _need("positions", positions, torch.int32, (T,))
+    return T, Hq, Hk, d, qs, ks, rot
+
+
+def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
+                          norm_eps=1e-6, interleaved=False, out=None, stream=None):
+    """RMS norm of every head of q [T, Hq, d] and k [T, Hk, d] (bf16 or fp32;
+    slices of a fused projection are taken as they are) with weights fp32 [d]
+    (None: ones), then the rotation of the first 2 * len(inv_freq) features by
+    positions int32 [T] * inv_freq fp32 (inv_freq None: no rotation).  k may
+    be None.  Returns (q, k); `out` = (q, k) may be the arguments themselves."""
+    T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight)
+    if out is None:
+        out = (torch.empty(T, Hq, d, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(T, Hk, d, dtype=q.dtype, device=q.device))
+    qo, ko = out
+    if qo.shape != q.shape or (k is not None and ko.shape != k.shape):
+        raise ValueError("outputs must have the inputs' shapes")
+    qos = _token_stride("q out", qo, T, q.dtype)
+    kos = 0 if k is None else _token_stride("k out", ko, T, q.dtype)
+    with _On(q, k, positions, inv_freq, q_weight, k_weight, qo, ko):
+        _check("diffattn_qk_norm_rope", load().diffattn_qk_norm_rope(
+            _ptr(q), qs, _ptr(k), ks, _dtype_code(q), T, Hq, Hk, d, _ptr(q_weight),
+            _ptr(k_weight), float(norm_eps), _ptr(positions), _ptr(inv_freq), rot,
+            int(bool(interleaved)), _ptr(qo), qos, _ptr(ko), kos, _stream(stream)))
+    return qo, ko
+
+
+def diffattn_qk_norm_rope_bwd_workspace_size(tokens, n_q_heads, n_k_heads, head_dim) -> int:
+    return int(load().diffattn_qk_norm_rope_bwd_workspace_size(tokens, n_q_heads, n_k_heads,
+                                                               head_dim))
+
+
+def diffattn_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, *, q_weight=None,
+                              k_weight=None, norm_eps=1e-6, interleaved=False, workspace=None,
+                              stream=None):
+    """Gradients of diffattn_qk_norm_rope: q, k are its inputs, dq_out, dk_out
+    (fp32) the gradients of its outputs.  Returns a dict of fp32 tensors: dq,
+    dk, dq_weight, dk_weight (None where the input is None)."""
+    T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight)
+    f32 = dict(dtype=torch.float32, device=q.device)
+    if dq_out.shape != q.shape or (k is not None and dk_out.shape != k.shape):
+        raise ValueError("the gradients must have the inputs' shapes")
+    gqs = _token_stride("dq_out", dq_out, T, torch.float32)
+    gks = 0 if k is None else _token_stride("dk_out", dk_out, T, torch.float32)
+    r = {"dq": torch.empty(T, Hq, d, **f32),
+         "dk": None if k is None else torch.empty(T, Hk, d, **f32),
+         "dq_weight": None if q_weight is None else torch.empty(d, **f32),
+         "dk_weight": None if k is None or k_weight is None else torch.empty(d, **f32)}
+    with _On(q, k, dq_out, dk_out, positions, inv_freq, q_weight, k_weight, workspace) as on:
+        ws, ws_bytes = _workspace(
+            workspace, diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), on.device, stream)
+        _check("diffattn_qk_norm_rope_bwd", load().diffattn_qk_norm_rope_bwd(
+            _ptr(q), qs, _ptr(k), ks, _dtype_code(q), _ptr(dq_out), gqs, _ptr(dk_out), gks, T, Hq,
+            Hk, d, _ptr(q_weight), _ptr(k_weight), float(norm_eps), _ptr(positions),
+            _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(r["dq"]), _ptr(r["dk"]),
+            _ptr(r["dq_weight"]), _ptr(r["dk_weight"]), _ptr(ws), ws_bytes, _stream(stream)))
+    return r
 
 
 def diffattn_reset_tile_counters(stream=None):

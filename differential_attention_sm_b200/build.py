@@ -25,9 +25,10 @@ FLAGS = [
 ]
 # The CUDA-core kernels in simt.cu serve the fp32 workload, whose accuracy
 # bound (1e-5 max abs) leaves no room for approximate exp, division and
-# square root: that file is built with IEEE-compliant math.  Every other file
+# square root: that file is built with IEEE-compliant math, and so is
+# qk_norm_rope.cu, whose fp32 rows are held to fp32's own steps.  Every other file
 # uses fast math (its exponentials are explicit ex2.approx or polynomial).
-PRECISE = {"simt.cu"}
+PRECISE = {"simt.cu", "qk_norm_rope.cu"}
 
 
 def flags_for(src: str):

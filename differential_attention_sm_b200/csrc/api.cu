@@ -114,6 +114,8 @@ const char* diffattn_status_string(int status) {
     case DA_ERR_CUDA: return "DA_ERR_CUDA";
     case DA_ERR_DEVICE_TIMEOUT: return "DA_ERR_DEVICE_TIMEOUT";
     case DA_ERR_SCHEDULE: return "DA_ERR_SCHEDULE";
+    case DA_ERR_PAGE: return "DA_ERR_PAGE";
+    case DA_ERR_CACHE_FULL: return "DA_ERR_CACHE_FULL";
     default: return "DA_ERR_UNKNOWN";
   }
 }

@@ -1,0 +1,745 @@
+// decode_kv4.cu — single-token differential attention over the paged 4-bit
+// cache (format and layout: kv4.cuh), V2 and V1.
+//
+//   S = q k^T / sqrt(d), o = O1 / l1 - lambda O2 / l2 with O = sum p v, l = sum p,
+//   p = 2^(s log2(e) - m), m a running reference maximum;  V1 then applies the
+//   per-head norm.
+//
+// Bound by the cache's bytes: 144 per token and KV head, and close behind by
+// the instructions that turn codes into operands.  So:
+//  - The work is one line of stages (32 tokens of one KV head of one
+//    sequence), computed from the lengths on the device and cut into equal
+//    runs, one for each warp of the grid: no lengths on the host, no idle
+//    warps behind ragged lengths, no synchronisation between warps.
+//  - Each warp keeps a ring of stages in shared memory filled by bulk copies
+//    (a page is contiguous, so a stage is one copy), which holds enough bytes
+//    in flight for the memory's latency.
+//  - The matrix instruction is m16n8k16 in fp16 with the cache as its 16-row
+//    operand: tokens x channels for the scores, channels x tokens for the
+//    values, the (at most 8) query heads as columns.  code * scale is exact in
+//    fp16, so the cache's values enter unrounded.  The layout gives every lane
+//    its own operand pieces: codes become fp16 pairs in its registers and
+//    never pass through shared memory again.  (tcgen05 would want them
+//    written back to shared or tensor memory first, and 16 columns at least;
+//    its rate is not what is missing here.)
+//  - q is scaled by a power of two per head into fp16's range (exact), p is
+//    rounded to fp16 (half a step is 2^-11 of a probability; the sums l and O
+//    are fp32).  m moves only when a score passes it by more than 2^10, so p
+//    reaches 2^15 at most and the common stage needs no maximum across lanes.
+// A run that ends or begins inside a sequence leaves (O, l, m) in the
+// workspace; a second kernel joins them, subtracts, and normalises.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "diffattn.h"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace da {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kStageTokens = 32;
+constexpr int kStageBytes = 2 * kKv4TileBytes;
+constexpr int kWarps = 4;
+constexpr int kRing = 3;
+constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSmWide = 3;  // two column tiles need more registers
+constexpr int kPlanSms = 148;      // fixed: the workspace size is the same on every device
+constexpr int kMinStages = 2;      // shortest run of a warp
+constexpr int kChunkHeads = 16;    // query heads that share one pass over the cache
+constexpr float kNoMax = -3.0e38f;
+constexpr float kShift = 5.0f;    // p = 2^(s - m + kShift)
+constexpr float kRaise = 10.0f;   // m is raised when a score passes m + kRaise
+
+struct Kv4Args {
+  const __nv_bfloat16* q;  // [batch][q_heads][128]
+  const uint8_t* cache;
+  const int* table;  // [batch][max_pages]
+  const int* lens;
+  int batch, heads, group, chunks;  // KV heads; query columns of one; passes over one
+  int max_pages, page_shift, n_pages, window;
+  float scale;  // log2(e) / sqrt(d)
+  int runs;     // warps of the grid
+  int cols;     // columns kept per slot
+  float* part_o;   // [slot][cols][128]
+  float* part_ml;  // [slot][cols][2]
+  int* dev_status;
+  // combine
+  const float* lambda;
+  __nv_bfloat16* out;
+  int out_heads, v1, apply_norm;
+  const float* gain;
+  float eps, post_scale;
+};
+
+constexpr int kSmemBytes = kWarps * kRing * (kStageBytes + 16);
+
+__device__ __forceinline__ void span_of(const Kv4Args& a, int b, int& lo, int& len) {
+  const long long room = (long long)a.max_pages << a.page_shift;
+  len = a.lens[b];
+  len = len < 0 ? 0 : (len > room ? (int)room : len);
+  lo = a.window > 0 && len > a.window ? len - a.window : 0;
+}
+__device__ __forceinline__ int stages_of(const Kv4Args& a, int b) {
+  int lo, len;
+  span_of(a, b, lo, len);
+  return len > lo ? (len - 1) / kStageTokens - lo / kStageTokens + 1 : 0;
+}
+
+// Stages of one (KV head, pass) of the sequences before `upto` (all of them
+// when it is the batch); the whole warp calls it.
+__device__ __forceinline__ long long stages_before(const Kv4Args& a, int upto) {
+  long long n = 0;
+  for (int b = (int)lane_id(); b < upto; b += 32) n += stages_of(a, b);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+  return n;
+}
+
+__device__ __forceinline__ long long run_length(const Kv4Args& a, long long total) {
+  const long long q = (total + a.runs - 1) / a.runs;
+  return q < kMinStages ? kMinStages : q;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+// Scale byte `i` of w in both halves; scale bytes `i`, `i + 1` in the halves.
+template <int i>
+__device__ __forceinline__ uint32_t scale_twice(uint32_t w) {
+  return __byte_perm(w, 0u, 0x0404u | (i << 4) | (i << 12)) >> 1;
+}
+template <int i>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w) {
+  return __byte_perm(w, 0u, 0x0404u | (i << 4) | ((i + 1) << 12)) >> 1;
+}
+
+// One warp's state of a segment: NT column tiles of 8 query heads.
+template <int NT>
+struct WarpState {
+  float o[NT][8][4];  // channels 16 * (lane / 4) + 2 * i, + 1; columns 2 * (lane % 4), + 1
+  float l[NT][2], m[NT][2];
+};
+
+// Sixteen tokens' scores: c[nt] holds tokens g, g + 8 of columns 2q, 2q + 1.
+template <int NT>
+__device__ __forceinline__ void tile_scores(uint32_t at, uint32_t lane, const uint32_t (&qf)[NT][16],
+                                            float (&c)[NT][4]) {
+  const uint4 k0 = lds128(at + lane * 16), k1 = lds128(at + 512 + lane * 16);
+  const uint32_t sw = lds32(at + kKv4KScales + lane * 4);
+  const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+  const uint32_t s00 = scale_twice<0>(sw), s01 = scale_twice<1>(sw), s10 = scale_twice<2>(sw),
+                 s11 = scale_twice<3>(sw);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t s0 = i < 2 ? s00 : s01, s1 = i < 2 ? s10 : s11;
+    uint32_t a[4], b[4];
+    e2m1x8_to_f16x2(w0[i], a[0], a[1], a[2], a[3]);
+    e2m1x8_to_f16x2(w1[i], b[0], b[1], b[2], b[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = hmul2(a[j], s0), b[j] = hmul2(b[j], s1);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mma_f16(c[n], a[0], b[0], a[1], b[1], qf[n][4 * i], qf[n][4 * i + 1]);
+      mma_f16(c[n], a[2], b[2], a[3], b[3], qf[n][4 * i + 2], qf[n][4 * i + 3]);
+    }
+  }
+}
+
+// Adds sixteen tokens' values: p[nt] are the operand's two registers.  `seen`
+// masks the scales of tokens that take no part (all ones for a whole tile): a
+// row behind the end may hold anything, and 0 * NaN is not 0.
+template <int NT>
+__device__ __forceinline__ void tile_values(uint32_t at, uint32_t lane, uint32_t seen0,
+                                            uint32_t seen1, const uint32_t (&p)[NT][2],
+                                            float (&o)[NT][8][4]) {
+  const uint4 v0 = lds128(at + kKv4VCodes + lane * 16),
+              v1 = lds128(at + kKv4VCodes + 512 + lane * 16);
+  const uint32_t sw = lds32(at + kKv4VScales + lane * 4);
+  const uint32_t s0 = scale_pair<0>(sw) & seen0, s1 = scale_pair<2>(sw) & seen1;
+  constexpr uint32_t kLow = 0x0F0F0F0Fu;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t x0 = half ? v0.y : v0.x, z0 = half ? v0.w : v0.z;
+    const uint32_t x1 = half ? v1.y : v1.x, z1 = half ? v1.w : v1.z;
+    // Bytes of (channel, channel + 1) of two tokens become bytes of (token,
+    // token + 1) of two channels.
+    uint32_t e0[4], d0[4], e1[4], d1[4];
+    e2m1x8_to_f16x2((x0 & kLow) | ((z0 << 4) & ~kLow), e0[0], e0[1], e0[2], e0[3]);
+    e2m1x8_to_f16x2(((x0 >> 4) & kLow) | (z0 & ~kLow), d0[0], d0[1], d0[2], d0[3]);
+    e2m1x8_to_f16x2((x1 & kLow) | ((z1 << 4) & ~kLow), e1[0], e1[1], e1[2], e1[3]);
+    e2m1x8_to_f16x2(((x1 >> 4) & kLow) | (z1 & ~kLow), d1[0], d1[1], d1[2], d1[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a0 = hmul2(e0[i], s0), a1 = hmul2(d0[i], s0), a2 = hmul2(e1[i], s1),
+                     a3 = hmul2(d1[i], s1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * half + i], a0, a1, a2, a3, p[n][0], p[n][1]);
+    }
+  }
+}
+
+template <int NT, bool kV1>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSmWide)
+    kv4_decode_kernel(const Kv4Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t lane = threadIdx.x & 31u;
+  const int warp = (int)(threadIdx.x >> 5);
+  const uint32_t g = lane >> 2, qd = lane & 3u;
+  uint8_t* ring = smem + warp * kRing * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * kRing * kStageBytes) + warp * kRing;
+  uint32_t* loaded = reinterpret_cast<uint32_t*>(smem + kWarps * kRing * (kStageBytes + 8)) +
+                     warp * kRing;  // which tiles of a ring slot hold tokens
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&bars[i], 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  const uint32_t ring_at = smem_u32(ring);
+
+  const int units = a.heads * a.chunks;  // of one sequence
+  const long long total = stages_before(a, a.batch) * units;
+  const long long run = run_length(a, total);
+  // Neighbouring runs lie on different SMs.
+  const int me = warp * (int)gridDim.x + (int)blockIdx.x;
+  long long pos = run * me;
+  const long long end = pos + run < total ? pos + run : total;
+  if (pos >= end) return;
+
+  // The sequence that holds `pos`.
+  int b = 0, n_b = 0;
+  long long base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int mine = b0 + (int)lane < a.batch ? stages_of(a, b0 + (int)lane) : 0;
+    long long upto = (long long)mine * units;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+      if ((int)lane >= off) upto += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + upto > pos);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      b = b0 + src;
+      n_b = __shfl_sync(0xffffffffu, mine, src);
+      base += __shfl_sync(0xffffffffu, upto, src) - (long long)n_b * units;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, upto, 31);
+  }
+
+  int slot = 0;          // next ring slot
+  uint32_t parity = 0;   // of that slot
+  bool failed = false;
+  while (pos < end) {
+    const int unit = (int)((pos - base) / n_b);
+    const int s_first = (int)((pos - base) - (long long)unit * n_b);
+    const int count = (int)(end - pos < n_b - s_first ? end - pos : n_b - s_first);
+    const int kvh = unit / a.chunks, chunk = unit - kvh * a.chunks;
+    int lo, len;
+    span_of(a, b, lo, len);
+    const int s0 = lo / kStageTokens + s_first;  // absolute stage
+
+    // Query fragments: column g of tile n, channels 32 * qd ...
+    uint32_t qf[NT][16];
+    float back[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = chunk * kChunkHeads + n * 8 + (int)g;
+      bool live = col < a.group;
+      const __nv_bfloat16* src;
+      if (kV1) {  // column 0 has features 0..63 of the head, column 1 the rest
+        src = a.q + ((size_t)b * a.heads + kvh) * kD + 32 * qd;
+        live = live && (g == qd / 2);
+      } else {
+        src = a.q + ((size_t)b * a.heads * a.group + (size_t)kvh * a.group + col) * kD + 32 * qd;
+      }
+      uint32_t raw[16];
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
+        raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        top = max(top, max((raw[i] << 16) & 0x7F800000u, raw[i] & 0x7F800000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // q * 2^-e is in fp16's range with e the largest exponent of the head.
+      // An exponent of 0 or of infinities is replaced: the products are 0 or
+      // not finite either way.
+      const uint32_t e = min(max(top >> 23, 1u), 253u);
+      const float down = __uint_as_float((254u - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        qf[n][i] = pack_f16(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
+      const float up = __uint_as_float(e << 23) * a.scale;
+      back[n][0] = __shfl_sync(0xffffffffu, up, 8 * qd);
+      back[n][1] = __shfl_sync(0xffffffffu, up, 8 * qd + 4);
+    }
+
+    WarpState<NT> w;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w.o[n][i][j] = 0.f;
+      w.l[n][0] = w.l[n][1] = 0.f;
+      w.m[n][0] = w.m[n][1] = kNoMax;
+    }
+
+    // Pages of 32 stages at a time, one stage per lane, the next 32 ahead.
+    const int* row = a.table + (size_t)b * a.max_pages;
+    const int first_tile = lo >> 4, last_tile = (len - 1) >> 4;
+    auto page_of = [&](int i, int half) {  // page of a tile of stage s0 + i; -1: not needed
+      const int tile = 2 * (s0 + i) + half;
+      return i < count && tile >= first_tile && tile <= last_tile
+                 ? row[tile >> (a.page_shift - 4)] : -1;
+    };
+    int pa = page_of((int)lane, 0), pb = page_of((int)lane, 1);
+    int na = page_of(32 + (int)lane, 0), nb = page_of(32 + (int)lane, 1);
+    const int64_t head_tiles = 1 << (a.page_shift - 4);
+    auto issue = [&](int i, int to) {  // stage i of the segment into ring slot `to`
+      const int ga = __shfl_sync(0xffffffffu, pa, i & 31), gb = __shfl_sync(0xffffffffu, pb, i & 31);
+      if (lane == 0) {
+        const int tile = 2 * (s0 + i);
+        const bool in_a = tile >= first_tile && tile <= last_tile;
+        const bool in_b = tile + 1 >= first_tile && tile + 1 <= last_tile;
+        const bool ok_a = in_a && (unsigned)ga < (unsigned)a.n_pages;
+        const bool ok_b = in_b && (unsigned)gb < (unsigned)a.n_pages;
+        if (in_a != ok_a || in_b != ok_b) report(a.dev_status, DA_ERR_PAGE);
+        loaded[to] = (ok_a ? 1u : 0u) | (ok_b ? 2u : 0u);
+        uint8_t* dst = ring + to * kStageBytes;
+        const int mask = (int)head_tiles - 1;
+        const uint8_t* src_a =
+            a.cache + (((int64_t)ga * a.heads + kvh) * head_tiles + (tile & mask)) * kKv4TileBytes;
+        const uint8_t* src_b =
+            a.cache +
+            (((int64_t)gb * a.heads + kvh) * head_tiles + ((tile + 1) & mask)) * kKv4TileBytes;
+        mbar_arrive_expect_tx(&bars[to], (ok_a ? kKv4TileBytes : 0) + (ok_b ? kKv4TileBytes : 0));
+        if (ok_a && ok_b && src_b == src_a + kKv4TileBytes) {
+          bulk_load(dst, src_a, kStageBytes, &bars[to]);
+        } else {
+          if (ok_a) bulk_load(dst, src_a, kKv4TileBytes, &bars[to]);
+          if (ok_b) bulk_load(dst + kKv4TileBytes, src_b, kKv4TileBytes, &bars[to]);
+        }
+      }
+    };
+    int issued = 0, to = slot;
+    for (; issued < kRing && issued < count; ++issued) {
+      issue(issued, to);
+      if (++to == kRing) to = 0;
+    }
+
+    for (int i = 0; i < count; ++i) {
+      mbar_wait(&bars[slot], parity, a.dev_status, &failed);
+      if (__any_sync(0xffffffffu, failed)) {
+        // Leave no copy of ours in flight: wait for the other slots, bounded too.
+        for (int k = i + 1; k < issued; ++k) {
+          if (++slot == kRing) slot = 0, parity ^= 1u;
+          failed = false;
+          mbar_wait(&bars[slot], parity, a.dev_status, &failed);
+        }
+        return;
+      }
+      const uint32_t at = ring_at + slot * kStageBytes;
+      const uint32_t have = loaded[slot];
+      float c[2][NT][4];
+      tile_scores<NT>(at, lane, qf, c[0]);
+      tile_scores<NT>(at + kKv4TileBytes, lane, qf, c[1]);
+      const int t0 = (s0 + i) * kStageTokens;
+      const bool whole = have == 3u && t0 >= lo && t0 + kStageTokens <= len;
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[t][n][j] *= back[n][j & 1];
+      }
+      uint32_t seen[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const bool there = (have >> t) & 1u;
+          auto sees = [&](int u) {
+            const int tok = t0 + 16 * t + u;
+            return there && tok >= lo && tok < len;
+          };
+          const bool r0 = sees((int)g), r1 = sees((int)g + 8);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (!r0) c[t][n][0] = c[t][n][1] = -INFINITY;
+            if (!r1) c[t][n][2] = c[t][n][3] = -INFINITY;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            seen[t][h] = (sees(2 * (int)qd + 8 * h) ? 0xFFFFu : 0u) |
+                         (sees(2 * (int)qd + 8 * h + 1) ? 0xFFFF0000u : 0u);
+        }
+      }
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mx[n][j] = max3(fmaxf(c[0][n][j], c[0][n][j + 2]), c[1][n][j], c[1][n][j + 2]);
+          raise |= mx[n][j] > w.m[n][j] + kRaise;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = mx[n][j];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(top, w.m[n][j]);
+            const float f = ex2(w.m[n][j] - top);
+            w.m[n][j] = top;
+            w.l[n][j] *= f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w.o[n][k][j] *= f, w.o[n][k][j + 2] *= f;
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = w.m[n][0] - kShift, m1 = w.m[n][1] - kShift;
+          const float p0 = ex2(c[t][n][0] - m0), p1 = ex2(c[t][n][1] - m1);
+          const float p2 = ex2(c[t][n][2] - m0), p3 = ex2(c[t][n][3] - m1);
+          w.l[n][0] += p0 + p2;
+          w.l[n][1] += p1 + p3;
+          p[n][0] = movmatrix_trans(pack_f16(p0, p1));
+          p[n][1] = movmatrix_trans(pack_f16(p2, p3));
+        }
+        tile_values<NT>(at + t * kKv4TileBytes, lane, seen[t][0], seen[t][1], p, w.o);
+      }
+      __syncwarp();  // every lane has read the slot
+      if (issued < count) {
+        issue(issued, slot);
+        if ((++issued & 31) == 0) {
+          pa = na, pb = nb;
+          na = page_of(issued + 32 + (int)lane, 0);
+          nb = page_of(issued + 32 + (int)lane, 1);
+        }
+      }
+      if (++slot == kRing) slot = 0, parity ^= 1u;
+    }
+    // The segment's sums.  Slots are ordered as the segments are: the next
+    // segment has the next unit or the next run.
+    const long long part = (long long)b * units + unit + me;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float l = w.l[n][j];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int col = n * 8 + 2 * (int)qd + j;
+        if (col < a.cols) {
+          float* dst = a.part_o + (part * a.cols + col) * kD + 16 * g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(dst)[i] =
+                make_float4(w.o[n][2 * i][j], w.o[n][2 * i][j + 2], w.o[n][2 * i + 1][j],
+                            w.o[n][2 * i + 1][j + 2]);
+          if (g == 0) {
+            float* ml = a.part_ml + (part * a.cols + col) * 2;
+            ml[0] = w.m[n][j];
+            ml[1] = l;
+          }
+        }
+      }
+    pos += count;
+    while (pos < end && pos >= base + (long long)n_b * units) {
+      base += (long long)n_b * units;
+      n_b = stages_of(a, ++b);
+    }
+  }
+}
+
+// One warp per output head: joins the segments of its two columns.
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const Kv4Args a) {
+  const int lane = (int)(threadIdx.x & 31);
+  const long long id = (long long)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  if (id >= (long long)a.batch * a.out_heads) return;
+  const int b = (int)(id / a.out_heads), p = (int)(id - (long long)b * a.out_heads);
+  int unit, col;
+  if (a.v1) {
+    unit = p;
+    col = 0;
+  } else {
+    const int kvh = 2 * p / a.group, at = 2 * p - kvh * a.group;
+    unit = kvh * a.chunks + at / kChunkHeads;
+    col = at % kChunkHeads;
+  }
+  const int units = a.heads * a.chunks;
+  const int n_b = stages_of(a, b);
+  const long long before = stages_before(a, b);
+  const long long run = run_length(a, stages_before(a, a.batch) * units);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (n_b > 0) {
+    const long long start = before * units + (long long)unit * n_b;
+    const int w0 = (int)(start / run), w1 = (int)((start + n_b - 1) / run);
+    const long long slot0 = (long long)b * units + unit + w0;
+    const int n = w1 - w0 + 1;
+    const float* ml = a.part_ml + (slot0 * a.cols + col) * 2;
+    const float* po = a.part_o + (slot0 * a.cols + col) * kD + 4 * lane;
+    const int64_t ml_step = 2 * a.cols, po_step = (int64_t)a.cols * kD;
+    float m[2] = {kNoMax, kNoMax};
+    for (int s = lane; s < n; s += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(ml + s * ml_step);
+      m[0] = fmaxf(m[0], v.x), m[1] = fmaxf(m[1], v.z);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], off));
+      m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], off));
+    }
+    float l[2] = {0.f, 0.f}, acc[2][4] = {};
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(ml + s * ml_step);
+      const float f0 = ex2(v.x - m[0]), f1 = ex2(v.z - m[1]);
+      const float4 x = *reinterpret_cast<const float4*>(po + s * po_step);
+      const float4 y = *reinterpret_cast<const float4*>(po + s * po_step + kD);
+      l[0] = fmaf(v.y, f0, l[0]), l[1] = fmaf(v.w, f1, l[1]);
+      acc[0][0] = fmaf(x.x, f0, acc[0][0]), acc[0][1] = fmaf(x.y, f0, acc[0][1]);
+      acc[0][2] = fmaf(x.z, f0, acc[0][2]), acc[0][3] = fmaf(x.w, f0, acc[0][3]);
+      acc[1][0] = fmaf(y.x, f1, acc[1][0]), acc[1][1] = fmaf(y.y, f1, acc[1][1]);
+      acc[1][2] = fmaf(y.z, f1, acc[1][2]), acc[1][3] = fmaf(y.w, f1, acc[1][3]);
+    }
+    const float lam = a.lambda[p];
+    // No token left by the mask: 0.
+    const float r0 = l[0] == 0.f ? 0.f : 1.f / l[0], r1 = l[1] == 0.f ? 0.f : lam / l[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = acc[0][i] * r0 - acc[1][i] * r1;
+    if (a.apply_norm) {
+      float ss = o[0] * o[0] + o[1] * o[1] + o[2] * o[2] + o[3] * o[3];
+#pragma unroll
+      for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      const float f = a.post_scale * rsqrtf(ss * (1.f / kD) + a.eps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] *= f * (a.gain ? a.gain[4 * lane + i] : 1.f);
+    }
+  }
+  *reinterpret_cast<uint2*>(a.out + id * kD + 4 * lane) =
+      make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int runs_of(int cols) {
+  return kPlanSms * (cols > 8 ? kCtasPerSmWide : kCtasPerSm) * kWarps;
+}
+
+size_t workspace_bytes_of(int batch, int units, int cols) {
+  const size_t slots = (size_t)batch * units + runs_of(cols);
+  return slots * cols * (kD + 2) * sizeof(float);
+}
+
+int chunks_of(int group) { return (group + kChunkHeads - 1) / kChunkHeads; }
+
+cudaError_t launch(Kv4Args& a, void* workspace, cudaStream_t stream) {
+  a.runs = runs_of(a.cols);
+  const size_t slots = (size_t)a.batch * a.heads * a.chunks + a.runs;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + slots * a.cols * kD;
+  const unsigned grid = (unsigned)(a.runs / kWarps);
+  auto run = [&](auto kernel) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kWarps * 32, kSmemBytes, stream>>>(a);
+    return cudaGetLastError();
+  };
+  cudaError_t e;
+  if (a.v1) e = run(kv4_decode_kernel<1, true>);
+  else if (a.cols <= 8) e = run(kv4_decode_kernel<1, false>);
+  else e = run(kv4_decode_kernel<2, false>);
+  if (e != cudaSuccess) return e;
+  const long long warps = (long long)a.batch * a.out_heads;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps));
+  cfg.blockDim = dim3(kCombineWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel, (const Kv4Args)a);
+}
+
+int check(const void* q, const void* cache, const int* table, const int* lens, const void* out,
+          const float* lambda, da_dtype dtype, int batch, int heads, int n_pages, int page_size,
+          int max_pages, int window) {
+  if (!q || !cache || !table || !lens || !out || !lambda) return DA_ERR_INVALID_ARG;
+  if (dtype != DA_BF16 && dtype != DA_FP32) return DA_ERR_INVALID_ARG;
+  if (batch < 1 || heads < 1 || n_pages < 1 || max_pages < 1 || page_size < 1 || window < 0)
+    return DA_ERR_INVALID_ARG;
+  if (dtype != DA_BF16 || !kv4_page_size_ok(page_size)) return DA_ERR_UNSUPPORTED;
+  if ((long long)n_pages * page_size >= (1LL << 31) ||
+      (long long)max_pages * page_size >= (1LL << 31))
+    return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+// Sizes whose indices fit the kernels'.
+bool sizes_ok(long long batch, long long q_heads) {
+  return batch <= (1 << 20) && q_heads <= (1 << 16) && batch * q_heads < (1LL << 28);
+}
+
+}  // namespace
+}  // namespace da
+
+using da::Kv4Args;
+
+extern "C" size_t diffattn_v2_decode_kv4_workspace_size(int batch, int n_q_heads,
+                                                        int n_kv_heads) {
+  if (batch < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads) return 0;
+  const int group = n_q_heads / n_kv_heads;
+  if (group % 2 || !da::sizes_ok(batch, n_q_heads)) return 0;
+  const int cols = group < da::kChunkHeads ? group : da::kChunkHeads;
+  return da::workspace_bytes_of(batch, n_kv_heads * da::chunks_of(group), cols);
+}
+
+extern "C" int diffattn_v2_decode_kv4(const void* q, const void* cache, int n_pages,
+                                      int page_size, const int* block_table, int max_pages,
+                                      const int* cache_lens, int window, void* out,
+                                      da_dtype dtype, int batch, int n_q_heads, int n_kv_heads,
+                                      int head_dim, const float* lambda, void* workspace,
+                                      size_t workspace_bytes, int* dev_status, void* stream) {
+  const int st = da::check(q, cache, block_table, cache_lens, out, lambda, dtype, batch,
+                           n_kv_heads, n_pages, page_size, max_pages, window);
+  if (st != DA_OK) return st;
+  if (n_q_heads < 1 || head_dim < 1 || n_q_heads % n_kv_heads || (n_q_heads / n_kv_heads) % 2)
+    return DA_ERR_INVALID_ARG;
+  if (head_dim != da::kD || !da::sizes_ok(batch, n_q_heads)) return DA_ERR_UNSUPPORTED;
+  if (!da::aligned16(q) || !da::aligned16(cache) || !da::aligned16(out)) return DA_ERR_ALIGNMENT;
+  if (!workspace ||
+      workspace_bytes < diffattn_v2_decode_kv4_workspace_size(batch, n_q_heads, n_kv_heads))
+    return DA_ERR_WORKSPACE;
+  if (!da::aligned16(workspace)) return DA_ERR_ALIGNMENT;
+  Kv4Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.table = block_table;
+  a.lens = cache_lens;
+  a.batch = batch;
+  a.heads = n_kv_heads;
+  a.group = n_q_heads / n_kv_heads;
+  a.chunks = da::chunks_of(a.group);
+  a.max_pages = max_pages;
+  a.page_shift = da::kv4_shift(page_size);
+  a.n_pages = n_pages;
+  a.window = window;
+  a.scale = (float)(1.4426950408889634 / std::sqrt(128.0));
+  a.cols = a.group < da::kChunkHeads ? a.group : da::kChunkHeads;
+  a.dev_status = dev_status;
+  a.lambda = lambda;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.out_heads = n_q_heads / 2;
+  return da::launch(a, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
+                                                                                    : DA_ERR_CUDA;
+}
+
+extern "C" size_t diffattn_v1_decode_kv4_workspace_size(int batch, int n_heads) {
+  if (batch < 1 || n_heads < 1 || !da::sizes_ok(batch, n_heads)) return 0;
+  return da::workspace_bytes_of(batch, n_heads, 2);
+}
+
+extern "C" int diffattn_v1_decode_kv4(const void* q, const void* cache, int n_pages,
+                                      int page_size, const int* block_table, int max_pages,
+                                      const int* cache_lens, int window, void* out,
+                                      da_dtype dtype, int batch, int n_heads, int d_qk, int d_v,
+                                      const float* lambda, int apply_norm,
+                                      const float* norm_weight, float norm_eps,
+                                      float lambda_init, void* workspace, size_t workspace_bytes,
+                                      int* dev_status, void* stream) {
+  const int st = da::check(q, cache, block_table, cache_lens, out, lambda, dtype, batch, n_heads,
+                           n_pages, page_size, max_pages, window);
+  if (st != DA_OK) return st;
+  if (d_qk < 1 || d_v < 1 || (apply_norm && !(norm_eps >= 0.f))) return DA_ERR_INVALID_ARG;
+  if (d_qk != 64 || d_v != da::kD || !da::sizes_ok(batch, n_heads)) return DA_ERR_UNSUPPORTED;
+  if (!da::aligned16(q) || !da::aligned16(cache) || !da::aligned16(out)) return DA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < diffattn_v1_decode_kv4_workspace_size(batch, n_heads))
+    return DA_ERR_WORKSPACE;
+  if (!da::aligned16(workspace)) return DA_ERR_ALIGNMENT;
+  Kv4Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.table = block_table;
+  a.lens = cache_lens;
+  a.batch = batch;
+  a.heads = n_heads;
+  a.group = 2;
+  a.chunks = 1;
+  a.max_pages = max_pages;
+  a.page_shift = da::kv4_shift(page_size);
+  a.n_pages = n_pages;
+  a.window = window;
+  a.scale = (float)(1.4426950408889634 / 8.0);
+  a.cols = 2;
+  a.dev_status = dev_status;
+  a.lambda = lambda;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.out_heads = n_heads;
+  a.v1 = 1;
+  a.apply_norm = apply_norm;
+  a.gain = norm_weight;
+  a.eps = norm_eps;
+  a.post_scale = 1.0f - lambda_init;
+  return da::launch(a, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK
+                                                                                    : DA_ERR_CUDA;
+}

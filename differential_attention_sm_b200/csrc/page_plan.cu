@@ -1,0 +1,382 @@
+// page_plan.cu — block table, slot map and positions of a step, from request
+// lengths on the device; and the return of finished requests' pages.
+//
+// With page size P, request r of old length l and n new tokens needs
+//     need_r = ceil((l + n) / P) - ceil(l / P)
+// further pages.  Let c_r be the inclusive sum of the needs.  The free pages
+// are a stack; request r takes its pages at depth c_r - need_r, so the result
+// depends on the request order alone.  r is served iff it fits its table row
+// and (n > 0) the slot rows, and need_r = 0 or c_r <= free: the sums never fall, so the
+// served takers are a prefix and their stack ranges do not overlap.
+//
+// Bound by latency: a step of 64 requests moves 2 KB.  One CTA does the sums
+// and all state, a row of requests per pass; with few slot rows it also writes
+// them, since every thread holds what its request needs.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "diffattn.h"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace da {
+namespace {
+
+constexpr int kMaxRequests = 1 << 16;
+
+struct PlanArgs {
+  const int* new_lens;
+  const int* lens;
+  int* table;
+  const int* stack;
+  const int* count;
+  int requests, max_pages, page_shift, n_pages, n_slots;
+  int* slots;
+  int* positions;
+  int* offsets;
+  int* served;
+  int* lens_out;
+  int* count_out;
+  int* dev_status;
+};
+
+// Inclusive sum over the block of one value per thread; `total` gets the sum.
+// `sh` holds 33 values; every thread of the block calls it.
+__device__ long long block_scan(long long x, long long* sh, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();  // the previous use of sh is over
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    const int n = (int)(blockDim.x >> 5);
+    long long y = lane < n ? sh[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long z = __shfl_up_sync(0xffffffffu, y, off);
+      if (lane >= off) y += z;
+    }
+    sh[lane] = y;
+  }
+  __syncthreads();
+  total = sh[(blockDim.x >> 5) - 1];
+  return x + (warp ? sh[warp - 1] : 0);
+}
+
+__device__ __forceinline__ int slot_of(int page, int pos, int shift) {
+  return (int)(((unsigned)page << shift) + (unsigned)(pos & ((1 << shift) - 1)));
+}
+
+// `with_slots`: this launch writes the slot rows too.
+__global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, int with_slots) {
+  __shared__ long long sh[33];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int ps = 1 << a.page_shift;
+  int free0 = *a.count;
+  free0 = free0 < 0 ? 0 : (free0 > a.n_pages ? a.n_pages : free0);
+  const long long room = (long long)a.max_pages << a.page_shift;
+  long long tok_base = 0, need_base = 0;
+  int taken = 0;         // the most pages that a served request reaches down to
+  bool refused = false;
+  for (int base = 0; base < a.requests; base += (int)blockDim.x) {
+    const int r = base + tid;
+    const bool live = r < a.requests;
+    int n = live ? a.new_lens[r] : 0;
+    n = n < 0 ? 0 : n;
+    int len = live ? a.lens[r] : 0;
+    len = len < 0 ? 0 : len;
+    long long tok_total, need_total;
+    const long long tok_end = tok_base + block_scan(n, sh, tok_total);
+    const long long tok_at = tok_end - n;
+    const long long after = (long long)len + n;
+    const bool fits = live && after <= room && (n == 0 || tok_end <= a.n_slots);
+    const int old = fits ? (int)(((long long)len + ps - 1) >> a.page_shift) : 0;
+    const int need = fits ? (int)((after + ps - 1) >> a.page_shift) - old : 0;
+    const long long upto = need_base + block_scan(need, sh, need_total);
+    const bool ok = fits && (need == 0 || upto <= free0);
+    if (ok && need) taken = max(taken, (int)upto);
+    refused |= live && !ok;
+    if (live) {
+      a.offsets[r] = (int)(tok_at < INT_MAX ? tok_at : INT_MAX);
+      if (r == a.requests - 1) a.offsets[r + 1] = (int)(tok_end < INT_MAX ? tok_end : INT_MAX);
+      a.served[r] = ok ? 1 : 0;
+      a.lens_out[r] = ok ? (int)after : len;
+    }
+    // New table entries and slot rows: a thread writes its own request's when
+    // they are few, else its whole warp does, one request at a time.
+    const int depth = (int)(upto - need);
+    const int rows = with_slots && live && tok_at < a.n_slots
+                         ? (int)(tok_end < a.n_slots ? n : a.n_slots - tok_at) : 0;
+    const int pages = ok ? need : 0;
+    const bool many = pages > 2 || rows > 2;
+    int* row = a.table + (size_t)(live ? r : 0) * a.max_pages;
+    if (!many) {
+      for (int j = 0; j < pages; ++j) row[old + j] = a.stack[free0 - 1 - (depth + j)];
+      for (int j = 0; j < rows; ++j) {
+        const int pos = (int)((unsigned)len + (unsigned)j), blk = pos >> a.page_shift;
+        int slot = -1;
+        if (ok)
+          slot = slot_of(blk < old ? row[blk] : a.stack[free0 - 1 - (depth + blk - old)], pos,
+                         a.page_shift);
+        a.slots[tok_at + j] = slot;
+        a.positions[tok_at + j] = pos;
+      }
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, many);
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int w_pages = __shfl_sync(0xffffffffu, pages, src);
+      const int w_rows = __shfl_sync(0xffffffffu, rows, src);
+      const int w_old = __shfl_sync(0xffffffffu, old, src);
+      const int w_depth = __shfl_sync(0xffffffffu, depth, src);
+      const int w_len = __shfl_sync(0xffffffffu, len, src);
+      const int w_ok = __shfl_sync(0xffffffffu, (int)ok, src);
+      const long long w_at = __shfl_sync(0xffffffffu, tok_at, src);
+      int* w_row = a.table + (size_t)(base + tid - lane + src) * a.max_pages;
+      for (int j = lane; j < w_pages; j += 32)
+        w_row[w_old + j] = a.stack[free0 - 1 - (w_depth + j)];
+      for (int j = lane; j < w_rows; j += 32) {
+        const int pos = (int)((unsigned)w_len + (unsigned)j), blk = pos >> a.page_shift;
+        int slot = -1;
+        if (w_ok)
+          slot = slot_of(
+              blk < w_old ? w_row[blk] : a.stack[free0 - 1 - (w_depth + blk - w_old)], pos,
+              a.page_shift);
+        a.slots[w_at + j] = slot;
+        a.positions[w_at + j] = pos;
+      }
+    }
+    tok_base += tok_total;
+    need_base += need_total;
+  }
+  if (with_slots) {  // rows behind the last token
+    for (long long i = tok_base + tid; i < a.n_slots; i += blockDim.x) {
+      a.slots[i] = -1;
+      a.positions[i] = 0;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, off));
+  __syncthreads();
+  int* top = reinterpret_cast<int*>(sh);
+  if (lane == 0) top[tid >> 5] = taken;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, top[w]);
+    *a.count_out = free0 - taken;
+  }
+  if (refused) report(a.dev_status, DA_ERR_CACHE_FULL);
+}
+
+// Slot rows of a large step: each thread finds its row's request by bisection
+// over the offsets.  A CTA bisects its first and last row once and then keeps
+// the offsets between them in shared memory when they fit.
+constexpr int kFillThreads = 256;
+constexpr int kFillRows = 2048;
+constexpr int kFillKeep = 1024;
+
+__device__ __forceinline__ int upper_request(const int* offsets, int lo, int hi, int i) {
+  // last r in [lo, hi] with offsets[r] <= i
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offsets[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs a) {
+  __shared__ int ends[2];
+  __shared__ int keep[kFillKeep];
+  const int first = blockIdx.x * kFillRows;
+  const int last = min(first + kFillRows, a.n_slots) - 1;
+  if (threadIdx.x < 2)
+    ends[threadIdx.x] = upper_request(a.offsets, 0, a.requests - 1, threadIdx.x ? last : first);
+  __syncthreads();
+  const int lo = ends[0], hi = ends[1];
+  const bool kept = hi - lo < kFillKeep;
+  if (kept)
+    for (int r = lo + threadIdx.x; r <= hi; r += kFillThreads) keep[r - lo] = a.offsets[r];
+  __syncthreads();
+  const int total = a.offsets[a.requests];
+  for (int i = first + threadIdx.x; i <= last; i += kFillThreads) {
+    int slot = -1, pos = 0;
+    if (i < total) {
+      const int r = kept ? lo + upper_request(keep, 0, hi - lo, i)
+                         : upper_request(a.offsets, lo, hi, i);
+      const int at = i - a.offsets[r];
+      const int ok = a.served[r];
+      int n = a.new_lens[r];
+      n = n < 0 ? 0 : n;
+      pos = (int)((unsigned)a.lens_out[r] - (unsigned)(ok ? n : 0) + (unsigned)at);
+      if (ok)
+        slot = slot_of(a.table[(size_t)r * a.max_pages + (pos >> a.page_shift)], pos,
+                       a.page_shift);
+    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
+  }
+}
+
+// Pages of the released requests go back on the stack in request order.
+struct ReleaseArgs {
+  const int* release;
+  int* lens;
+  int* table;
+  int* stack;
+  int* count;
+  int requests, max_pages, page_shift, n_pages;
+  int* dev_status;
+};
+
+__global__ void __launch_bounds__(1024) page_release_kernel(const ReleaseArgs a) {
+  __shared__ long long sh[33];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int ps = 1 << a.page_shift;
+  int free0 = *a.count;
+  free0 = free0 < 0 ? 0 : (free0 > a.n_pages ? a.n_pages : free0);
+  long long at_base = free0;
+  bool bad = false;
+  for (int base = 0; base < a.requests; base += (int)blockDim.x) {
+    const int r = base + tid;
+    const bool out = r < a.requests && a.release[r] != 0;
+    int pages = 0;
+    if (out) {
+      const int len = a.lens[r];
+      const long long p = len > 0 ? ((long long)len + ps - 1) >> a.page_shift : 0;
+      pages = (int)(p < a.max_pages ? p : a.max_pages);
+      a.lens[r] = 0;
+    }
+    // A warp takes its requests one at a time: first it counts the entries
+    // that are pages (others are left out), then it moves them.
+    int good = 0;
+    for (unsigned todo = __ballot_sync(0xffffffffu, pages > 0); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int n = __shfl_sync(0xffffffffu, pages, src);
+      const int* mine = a.table + (size_t)(base + tid - lane + src) * a.max_pages;
+      int c = 0;
+      for (int j = lane; j < n; j += 32) c += (unsigned)mine[j] < (unsigned)a.n_pages;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == src) good = c;
+    }
+    bad |= good < pages;
+    long long total;
+    const long long at = at_base + block_scan(good, sh, total) - good;
+    for (unsigned todo = __ballot_sync(0xffffffffu, pages > 0); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int n = __shfl_sync(0xffffffffu, pages, src);
+      long long to = __shfl_sync(0xffffffffu, at, src);
+      int* row = a.table + (size_t)(base + tid - lane + src) * a.max_pages;
+      for (int j0 = 0; j0 < n; j0 += 32) {
+        const int j = j0 + lane;
+        const int page = j < n ? row[j] : -1;
+        if (j < n) row[j] = -1;
+        const bool ok = (unsigned)page < (unsigned)a.n_pages;
+        const unsigned put = __ballot_sync(0xffffffffu, ok);
+        const long long where = to + __popc(put & ((1u << lane) - 1u));
+        if (ok && where < a.n_pages) a.stack[where] = page;
+        bad |= ok && where >= a.n_pages;
+        to += __popc(put);
+      }
+    }
+    at_base += total;
+  }
+  if (tid == 0) *a.count = (int)(at_base < a.n_pages ? at_base : a.n_pages);
+  if (bad) report(a.dev_status, DA_ERR_PAGE);
+}
+
+int threads_for(int requests) {
+  int t = 32;
+  while (t < requests && t < 1024) t <<= 1;
+  return t;
+}
+
+int check(int requests, int max_pages, int n_pages, int page_size) {
+  if (requests < 1 || max_pages < 1 || n_pages < 1 || page_size < 1) return DA_ERR_INVALID_ARG;
+  if (!kv4_page_size_ok(page_size) || requests > kMaxRequests) return DA_ERR_UNSUPPORTED;
+  if ((long long)n_pages * page_size >= (1LL << 31) ||
+      (long long)max_pages * page_size >= (1LL << 31))
+    return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+
+// Slot rows that the one CTA of the plan still writes itself.
+constexpr int kOneCtaRows = 4096;
+
+}  // namespace
+}  // namespace da
+
+extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, int* block_table,
+                                  const int* free_pages, const int* free_count, int requests,
+                                  int max_pages, int n_pages, int page_size, int n_slots,
+                                  int* slots, int* positions, int* offsets, int* served,
+                                  int* cache_lens_out, int* free_count_out, int* dev_status,
+                                  void* stream) {
+  if (!new_lens || !cache_lens || !block_table || !free_pages || !free_count || !offsets ||
+      !served || !cache_lens_out || !free_count_out)
+    return DA_ERR_INVALID_ARG;
+  if (n_slots < 0 || (n_slots > 0 && (!slots || !positions))) return DA_ERR_INVALID_ARG;
+  const int st = da::check(requests, max_pages, n_pages, page_size);
+  if (st != DA_OK) return st;
+  if (n_slots > (1 << 30)) return DA_ERR_UNSUPPORTED;
+  da::PlanArgs a{};
+  a.new_lens = new_lens;
+  a.lens = cache_lens;
+  a.table = block_table;
+  a.stack = free_pages;
+  a.count = free_count;
+  a.requests = requests;
+  a.max_pages = max_pages;
+  a.page_shift = da::kv4_shift(page_size);
+  a.n_pages = n_pages;
+  a.n_slots = n_slots;
+  a.slots = slots;
+  a.positions = positions;
+  a.offsets = offsets;
+  a.served = served;
+  a.lens_out = cache_lens_out;
+  a.count_out = free_count_out;
+  a.dev_status = dev_status;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int one = n_slots <= da::kOneCtaRows;
+  da::page_plan_kernel<<<1, da::threads_for(requests), 0, cs>>>(a, one);
+  if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
+  if (!one) {
+    const unsigned grid = (unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows);
+    da::page_slots_kernel<<<grid, da::kFillThreads, 0, cs>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
+  }
+  return DA_OK;
+}
+
+extern "C" int diffattn_page_release(const int* release, int* cache_lens, int* block_table,
+                                     int* free_pages, int* free_count, int requests,
+                                     int max_pages, int n_pages, int page_size, int* dev_status,
+                                     void* stream) {
+  if (!release || !cache_lens || !block_table || !free_pages || !free_count)
+    return DA_ERR_INVALID_ARG;
+  const int st = da::check(requests, max_pages, n_pages, page_size);
+  if (st != DA_OK) return st;
+  da::ReleaseArgs a{};
+  a.release = release;
+  a.lens = cache_lens;
+  a.table = block_table;
+  a.stack = free_pages;
+  a.count = free_count;
+  a.requests = requests;
+  a.max_pages = max_pages;
+  a.page_shift = da::kv4_shift(page_size);
+  a.n_pages = n_pages;
+  a.dev_status = dev_status;
+  da::page_release_kernel<<<1, da::threads_for(requests), 0,
+                            static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}

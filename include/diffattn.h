@@ -72,8 +72,11 @@ typedef enum {
   DA_ERR_WORKSPACE = -4,     /* workspace missing or smaller than required */
   DA_ERR_CUDA = -5,          /* a CUDA runtime/driver call or launch failed */
   DA_ERR_DEVICE_TIMEOUT = -6, /* written to dev_status by a kernel whose wait timed out */
-  DA_ERR_SCHEDULE = -7        /* written to dev_status by a prefill launch whose tile
+  DA_ERR_SCHEDULE = -7,       /* written to dev_status by a prefill launch whose tile
                                  counter another launch held for longer than 2 s */
+  DA_ERR_PAGE = -8,           /* written to dev_status: a page or slot index out of range */
+  DA_ERR_CACHE_FULL = -9      /* written to dev_status by diffattn_page_plan when a request
+                                 was not served */
 } da_status;
 
 typedef enum { DA_BF16 = 0, DA_FP32 = 1 } da_dtype;
@@ -399,6 +402,182 @@ DA_API int diffattn_v2_prefill_oproj(const void* q, const void* k, const void* v
                                      int n_kv_heads, int head_dim, int d_model, int causal,
                                      int window, void* workspace, size_t workspace_bytes,
                                      int* dev_status, void* stream);
+
+/* ---- Paged 4-bit KV cache ---------------------------------------------------
+ * No counterpart on the pages (they define the operator, not how a server
+ * keeps its cache).  A step of a serving loop is
+ *     diffattn_page_plan       pages and slots of the step's new tokens
+ *     diffattn_qk_norm_rope    norms and rotates the new queries and keys
+ *     diffattn_kv4_append      writes the new K/V rows into the cache
+ *     diffattn_v*_decode_kv4   attends over the cache
+ * and nothing in it is read back to the host.
+ *
+ * Cache: device uint8 [n_pages][n_kv_heads][page_size * 144], 16-byte
+ * aligned; page_size a power of two, 16 .. 1024.  A row (128 channels of one
+ * token's K or V in one KV head) is 8 blocks of 16 channels: one scale byte
+ * and sixteen 4-bit codes each, 4.5 bits per value.
+ *   code : sign bit, then 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scale: byte b is the fp16 number with bits b << 7 (5 exponent and 3
+ *          mantissa bits), b <= 0xE2 (10240): the nearest such number to
+ *          amax / 6, ties to even; 0xFF (a NaN) marks a block that held a NaN
+ *          or an infinity, and every value of it reads back as NaN.
+ *   x is held as the level nearest to x / scale (ties to the even code,
+ *   magnitudes above 6 * scale as 6) times scale, which is exact in bf16.
+ * Rows lie in tiles of 16 tokens of a head (2304 bytes: K codes, V codes, K
+ * scales, V scales; page_size / 16 tiles in a row).  Within a tile, token t,
+ * channel c, block b = c / 16:
+ *   K code  byte t * 64 + c / 2 (even channels in the low four bits)
+ *   V code  byte 1024 + 512 * (t / 8) + 64 * b + 16 * ((t % 8) / 2)
+ *                + 8 * (t % 2) + (c % 16) / 2
+ *   K scale byte 2048 + 16 * (t % 8) + 4 * (b / 2) + 2 * (t / 8) + b % 2
+ *   V scale byte 2176 + 16 * b + 4 * ((t % 8) / 2) + 2 * (t / 8) + t % 2
+ * A V1 head's K row is its two 64-wide branches.
+ *
+ * Slot: page * page_size + (position % page_size); a negative slot means no
+ * row.  block_table: device int32 [n][max_pages], row r the pages of request
+ * r in order of position; only its first ceil(length / page_size) entries are
+ * read.  n_pages * page_size and max_pages * page_size are below 2^31.
+ *
+ * Indices that come from device memory are checked there: a page or slot out
+ * of range is skipped, and DA_ERR_PAGE is stored in dev_status (optional). */
+
+/* Bytes of one page of the cache; 0 for sizes that are not supported. */
+DA_API size_t diffattn_kv4_page_bytes(int n_kv_heads, int head_dim, int page_size);
+
+/* Block table, slot map and positions of a step, from request lengths.
+ * Request r has cache_lens[r] tokens in the cache and new_lens[r] new ones
+ * (negative values count as 0).  It is served if
+ *   - cache_lens[r] + new_lens[r] <= max_pages * page_size,
+ *   - it has no new tokens, or they end within the n_slots slot rows, and
+ *   - the free pages suffice for it after the requests before it: needs are
+ *     summed over r in order, those of requests refused for lack of pages
+ *     included; a request that needs no further page passes this.
+ * Free pages are a stack, free_pages[0 .. *free_count), used from its end.
+ *   block_table   : int32 [requests][max_pages], the new pages are written in
+ *                   place behind the old ones; nothing else of it changes
+ *   free_pages    : int32 [n_pages], only read
+ *   free_count    : int32 [1], only read (clamped to 0 .. n_pages)
+ *   slots         : int32 [n_slots], slot of each new token, requests in
+ *                   order; -1 for tokens of requests that are not served and
+ *                   for rows behind the last token
+ *   positions     : int32 [n_slots], the tokens' positions; 0 behind the last
+ *   offsets       : int32 [requests + 1], first slot row of each request (at
+ *                   most 2^31 - 1), and their end
+ *   served        : int32 [requests], 1 or 0
+ *   cache_lens_out: int32 [requests], the length after the step (the old one
+ *                   if not served); may be cache_lens
+ *   free_count_out: int32 [1], pages left; may be free_count
+ * All device pointers.  slots and positions may be NULL with n_slots = 0.
+ * Up to 65536 requests and 2^30 slot rows.  DA_ERR_CACHE_FULL goes to dev_status if a request
+ * was not served.  The result depends on the arguments' values alone, and a
+ * call repeated with the same ones writes the same. */
+DA_API int diffattn_page_plan(const int* new_lens, const int* cache_lens, int* block_table,
+                              const int* free_pages, const int* free_count, int requests,
+                              int max_pages, int n_pages, int page_size, int n_slots, int* slots,
+                              int* positions, int* offsets, int* served, int* cache_lens_out,
+                              int* free_count_out, int* dev_status, void* stream);
+
+/* Gives the pages of finished requests back: for each r with release[r] != 0,
+ * in order, its ceil(cache_lens[r] / page_size) pages go on the stack, their
+ * table entries become -1 and cache_lens[r] becomes 0.  Entries that are no
+ * page (DA_ERR_PAGE) are left out.  All device pointers, changed in place. */
+DA_API int diffattn_page_release(const int* release, int* cache_lens, int* block_table,
+                                 int* free_pages, int* free_count, int requests, int max_pages,
+                                 int n_pages, int page_size, int* dev_status, void* stream);
+
+/* Writes rows into the cache.  k, v: device bf16 or fp32, token t's row of
+ * head h at t * token_stride + h * head_dim (strides in elements, at least
+ * n_kv_heads * head_dim and a multiple of 16 bytes: slices of a fused
+ * projection are taken as they are).  slots: device int32 [tokens]; a token
+ * with a negative slot is skipped.  Two tokens of one call must not have the
+ * same slot.  head_dim = 128 only (DA_ERR_UNSUPPORTED otherwise). */
+DA_API int diffattn_kv4_append(const void* k, long long k_token_stride, const void* v,
+                               long long v_token_stride, da_dtype dtype, const int* slots,
+                               int tokens, int n_kv_heads, int head_dim, void* cache,
+                               int n_pages, int page_size, int* dev_status, void* stream);
+
+/* Reads rows back: k, v: device [tokens][n_kv_heads][head_dim], bf16 or fp32
+ * (both exact).  Rows of tokens with a negative slot are left as they were. */
+DA_API int diffattn_kv4_read(const void* cache, int n_pages, int page_size, const int* slots,
+                             int tokens, int n_kv_heads, int head_dim, void* k, void* v,
+                             da_dtype dtype, int* dev_status, void* stream);
+
+/* Single-token decode over the 4-bit cache: the operator of
+ * diffattn_v2_decode_window and diffattn_v1_decode_window with the cache
+ * above.  Sequence b attends the last min(window, cache_lens[b]) of its
+ * cache_lens[b] tokens (window = 0: all; lengths are clamped to
+ * 0 .. max_pages * page_size on the device).  A sequence without tokens
+ * gives 0.  Tokens on a page out of range take no part (DA_ERR_PAGE).
+ *   q           : device bf16 [batch][n_q_heads][128] (V1: [batch][n_heads][2 * d_qk])
+ *   out         : device bf16 [batch][n_q_heads / 2][128] (V1: [batch][n_heads][d_v])
+ *   cache_lens  : device int32 [batch]
+ *   workspace   : 16-byte aligned scratch of the queried size, which does not
+ *                 depend on the lengths.  Calls that may overlap need one each.
+ * Supported: bf16; V2 head_dim = 128 with any even n_q_heads / n_kv_heads (up
+ * to 16 query heads share one pass over the cache); V1 d_qk = 64, d_v = 128.
+ * Other errors as for the dense calls.  The result does not depend on the
+ * pages' order, and equal calls give equal bits. */
+DA_API size_t diffattn_v2_decode_kv4_workspace_size(int batch, int n_q_heads, int n_kv_heads);
+DA_API int diffattn_v2_decode_kv4(const void* q, const void* cache, int n_pages, int page_size,
+                                  const int* block_table, int max_pages, const int* cache_lens,
+                                  int window, void* out, da_dtype dtype, int batch,
+                                  int n_q_heads, int n_kv_heads, int head_dim,
+                                  const float* lambda, void* workspace, size_t workspace_bytes,
+                                  int* dev_status, void* stream);
+DA_API size_t diffattn_v1_decode_kv4_workspace_size(int batch, int n_heads);
+DA_API int diffattn_v1_decode_kv4(const void* q, const void* cache, int n_pages, int page_size,
+                                  const int* block_table, int max_pages, const int* cache_lens,
+                                  int window, void* out, da_dtype dtype, int batch, int n_heads,
+                                  int d_qk, int d_v, const float* lambda, int apply_norm,
+                                  const float* norm_weight, float norm_eps, float lambda_init,
+                                  void* workspace, size_t workspace_bytes, int* dev_status,
+                                  void* stream);
+
+/* ---- Norm of queries and keys with the position rotation --------------------
+ * No counterpart on the pages.  For every query and key head (V1: call it
+ * with 2 * n_heads heads of width d_qk to norm and turn each branch):
+ *     n = x / sqrt(mean(x^2) + norm_eps) * w
+ * then the first rot_dim features are rotated in pairs (a, b) by the angle
+ * positions[t] * inv_freq[i], i < rot_dim / 2:
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ * Pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved != 0.
+ *   q, k        : device bf16 or fp32, token t's head h at t * token_stride +
+ *                 h * head_dim (elements; at least heads * head_dim, multiples
+ *                 of 16 bytes).  n_k_heads = 0: no keys (k may be NULL).
+ *   q_out, k_out: same type, strides of their own; may be q and k themselves
+ *                 with the same strides, otherwise must not overlap them
+ *   q_weight, k_weight: device fp32 [head_dim], 16-byte aligned, or NULL (ones)
+ *   positions   : device int32 [tokens]; inv_freq: device fp32 [rot_dim / 2];
+ *                 both may be NULL with rot_dim = 0 (norm only)
+ * Angles are formed in 64 bits.  head_dim and rot_dim multiples of 16,
+ * head_dim <= 256 (DA_ERR_UNSUPPORTED otherwise). */
+DA_API int diffattn_qk_norm_rope(const void* q, long long q_token_stride, const void* k,
+                                 long long k_token_stride, da_dtype dtype, int tokens,
+                                 int n_q_heads, int n_k_heads, int head_dim,
+                                 const float* q_weight, const float* k_weight, float norm_eps,
+                                 const int* positions, const float* inv_freq, int rot_dim,
+                                 int interleaved, void* q_out, long long q_out_token_stride,
+                                 void* k_out, long long k_out_token_stride, void* stream);
+
+/* Its gradients.  q, k are the forward's inputs; dq_out, dk_out (device fp32,
+ * strides as above) the gradients of its outputs, as diffattn_v*_bwd writes
+ * them.  Outputs (device fp32, dense, written, not accumulated): dq, dk like
+ * q, k; dq_weight, dk_weight [head_dim], or NULL.  dq may be dq_out and dk
+ * dk_out if those are dense.  The weights' gradients are summed in a fixed
+ * order: equal calls give equal bits.  workspace: 16-byte aligned scratch of
+ * the queried size. */
+DA_API size_t diffattn_qk_norm_rope_bwd_workspace_size(int tokens, int n_q_heads, int n_k_heads,
+                                                       int head_dim);
+DA_API int diffattn_qk_norm_rope_bwd(const void* q, long long q_token_stride, const void* k,
+                                     long long k_token_stride, da_dtype dtype,
+                                     const float* dq_out, long long dq_out_token_stride,
+                                     const float* dk_out, long long dk_out_token_stride,
+                                     int tokens, int n_q_heads, int n_k_heads, int head_dim,
+                                     const float* q_weight, const float* k_weight,
+                                     float norm_eps, const int* positions, const float* inv_freq,
+                                     int rot_dim, int interleaved, float* dq, float* dk,
+                                     float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* ---- Tile counters of the tensor-core prefill ------------------------------
  * No counterpart on the pages (they are this library's scheduling state).

@@ -648,67 +648,102 @@ def diffattn_selftest_wait_timeout(timeout_us, dev_status, waited_ns=None, strea
 
 
 # ---- serving: page plan, 4-bit paged cache, decode over it; QK norm + rotation
-class _On:
-    """The device of a call: checks that its tensors lie on it, makes it
-    current for the call, and gives the stream."""
-
-    def __init__(self, first, *others):
-        if not first.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        self.device = first.device
-        for t in others:
-            if t is not None and t.device != self.device:
-                raise ValueError("tensors lie on different devices (%s, %s)"
-                                 % (self.device, t.device))
-        self._guard = torch.cuda.device(self.device)
-
-    def __enter__(self):
-        self._guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+# These calls take microseconds on the GPU, so the checks here are the cheap
+# forms: one comparison each, device indices instead of device objects, and the
+# device is only switched when it is not the current one.
+_I32, _U8, _F32, _BF16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
+_CODES = {_BF16: DA_BF16, _F32: DA_FP32}
 
 
 def _need(name, t, dtype, shape=None):
-    """A dense tensor of one type (and, entries of None aside, shape)."""
-    if t.dtype != dtype:
+    """A dense tensor of one type and shape (None: any)."""
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and (t.dim() != len(shape) or any(
-            want is not None and want != have for want, have in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+
+
+def _one_device(first, *others):
+    """Index of the device that all tensors of a call lie on."""
+    at = first.get_device()
+    if at < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError("tensors lie on different devices (cuda:%d, %s)" % (at, t.device))
+    return at
+
+
+def _run(name, at, stream, *args):
+    """Calls an entry point with device `at` current, on `stream` (None: that
+    device's current stream)."""
+    fn = getattr(load(), name)
+    if torch._C._cuda_getDevice() != at:
+        with torch.cuda.device(at):
+            status = fn(*args, _stream(stream))
+    else:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None
+                    else _stream(stream))
+    if status != DA_OK:
+        raise DiffAttnError(name, status)
 
 
 def _token_stride(name, t, tokens=None, dtype=None):
     """Token stride of t [T, H, d], whose heads of a token lie in a row."""
     if t.dim() != 3 or (tokens is not None and t.shape[0] != tokens):
         raise ValueError("%s must be [tokens, heads, width], got %s" % (name, tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
     T, H, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d):
         raise ValueError("%s: the heads of a token must lie in a row" % name)
-    return t.stride(0) if T > 1 else max(1, H) * d
+    return st if T > 1 else max(1, H) * d
 
 
-def _workspace(workspace, need, device, stream):
+def _code(name, t):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s: unsupported dtype %s" % (name, t.dtype))
+    return code
+
+
+def _workspace(workspace, need, at, stream):
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        device = torch.device("cuda", at)
+        workspace = torch.empty(max(need, 1), dtype=_U8, device=device)
         if stream is not None:   # freed on return: kept from reuse until that stream is past it
             workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace
 
 
-def _kv4_cache(cache, n_kv_heads=None):
+def _kv4_cache(cache):
     """(pages, KV heads, page size) of a cache [n_pages, n_kv_heads, page_size * 144]."""
-    _need("cache", cache, torch.uint8, (None, n_kv_heads, None))
-    if cache.shape[2] % 144:
-        raise ValueError("cache must be [n_pages, n_kv_heads, page_size * 144]")
-    return cache.shape[0], cache.shape[1], cache.shape[2] // 144
+    _need("cache", cache, _U8)
+    if cache.dim() != 3 or cache.shape[2] % 144:
+        raise ValueError("cache must be [n_pages, n_kv_heads, page_size * 144], not %s"
+                         % (tuple(cache.shape),))
+    pages, heads, nbytes = cache.shape
+    return pages, heads, nbytes // 144
+
+
+def _page_lists(first, cache_lens, block_table, free_pages, free_count):
+    """(requests, max_pages, n_pages), all checked."""
+    R = first.numel()
+    _need("cache_lens", cache_lens, _I32, (R,))
+    _need("block_table", block_table, _I32)
+    _need("free_pages", free_pages, _I32)
+    _need("free_count", free_count, _I32, (1,))
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [%d, max_pages], not %s"
+                         % (R, tuple(block_table.shape)))
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [n_pages]")
+    return R, block_table.shape[1], free_pages.shape[0]
 
 
 def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count, page_size,
@@ -720,33 +755,29 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
     [R + 1], served, cache_lens [R], free_count [1] (int32).  `out`, such a
     dict, is written instead of new tensors; its cache_lens and free_count
     may be the arguments themselves."""
-    i32 = torch.int32
-    R = new_lens.numel()
-    _need("new_lens", new_lens, i32, (R,))
-    _need("cache_lens", cache_lens, i32, (R,))
-    _need("block_table", block_table, i32, (R, None))
-    _need("free_pages", free_pages, i32, (None,))
-    _need("free_count", free_count, i32, (1,))
-    sizes = {"slots": n_slots, "positions": n_slots, "offsets": R + 1, "served": R,
-             "cache_lens": R, "free_count": 1}
+    R, max_pages, n_pages = _page_lists(new_lens, cache_lens, block_table, free_pages, free_count)
+    _need("new_lens", new_lens, _I32, (R,))
+    if n_slots < 0:
+        raise ValueError("n_slots is negative")
     if out is None:
-        # one allocation; the pieces start on 16-byte boundaries
-        at, total = {}, 0
-        for name, n in sizes.items():
-            at[name] = total
-            total += (n + 3) // 4 * 4
-        flat = torch.empty(total, dtype=i32, device=new_lens.device)
-        out = {name: flat[at[name]:at[name] + n] for name, n in sizes.items()}
-    for name, n in sizes.items():
-        _need(name, out[name], i32, (n,))
-    with _On(new_lens, cache_lens, block_table, free_pages, free_count, dev_status,
-             *out.values()):
-        _check("diffattn_page_plan", load().diffattn_page_plan(
-            _ptr(new_lens), _ptr(cache_lens), _ptr(block_table), _ptr(free_pages),
-            _ptr(free_count), R, block_table.shape[1], free_pages.numel(), int(page_size),
-            int(n_slots), _ptr(out["slots"]), _ptr(out["positions"]), _ptr(out["offsets"]),
-            _ptr(out["served"]), _ptr(out["cache_lens"]), _ptr(out["free_count"]),
-            _ptr(dev_status), _stream(stream)))
+        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, dev_status)
+        slots, positions, offsets, served, lens, count = torch.empty(
+            2 * n_slots + 3 * R + 2, dtype=_I32, device=new_lens.device).split_with_sizes(
+                (n_slots, n_slots, R + 1, R, R, 1))
+        out = {"slots": slots, "positions": positions, "offsets": offsets, "served": served,
+               "cache_lens": lens, "free_count": count}
+    else:
+        for name, n in (("slots", n_slots), ("positions", n_slots), ("offsets", R + 1),
+                        ("served", R), ("cache_lens", R), ("free_count", 1)):
+            _need(name, out[name], _I32, (n,))
+        slots, positions, offsets, served, lens, count = (out[name] for name in (
+            "slots", "positions", "offsets", "served", "cache_lens", "free_count"))
+        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, dev_status,
+                         slots, positions, offsets, served, lens, count)
+    _run("diffattn_page_plan", at, stream, new_lens.data_ptr(), cache_lens.data_ptr(),
+         block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
+         n_pages, page_size, n_slots, slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
+         served.data_ptr(), lens.data_ptr(), count.data_ptr(), _ptr(dev_status))
     return out
 
 
@@ -754,18 +785,12 @@ def diffattn_page_release(release, cache_lens, block_table, free_pages, free_cou
                           dev_status=None, stream=None):
     """Gives the pages of requests with release[r] != 0 back (int32 [R]);
     cache_lens, block_table, free_pages and free_count are changed in place."""
-    i32 = torch.int32
-    R = release.numel()
-    _need("release", release, i32, (R,))
-    _need("cache_lens", cache_lens, i32, (R,))
-    _need("block_table", block_table, i32, (R, None))
-    _need("free_pages", free_pages, i32, (None,))
-    _need("free_count", free_count, i32, (1,))
-    with _On(release, cache_lens, block_table, free_pages, free_count, dev_status):
-        _check("diffattn_page_release", load().diffattn_page_release(
-            _ptr(release), _ptr(cache_lens), _ptr(block_table), _ptr(free_pages),
-            _ptr(free_count), R, block_table.shape[1], free_pages.numel(), int(page_size),
-            _ptr(dev_status), _stream(stream)))
+    R, max_pages, n_pages = _page_lists(release, cache_lens, block_table, free_pages, free_count)
+    _need("release", release, _I32, (R,))
+    at = _one_device(release, cache_lens, block_table, free_pages, free_count, dev_status)
+    _run("diffattn_page_release", at, stream, release.data_ptr(), cache_lens.data_ptr(),
+         block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
+         n_pages, page_size, _ptr(dev_status))
 
 
 def diffattn_kv4_page_bytes(n_kv_heads, head_dim, page_size) -> int:
@@ -776,16 +801,18 @@ def diffattn_kv4_append(k, v, slots, cache, *, dev_status=None, stream=None):
     """Writes rows k, v [T, Hkv, 128] (bf16 or fp32; slices of a fused
     projection are taken as they are) into the 4-bit cache
     [n_pages, Hkv, page_size * 144] uint8 at slots int32 [T] (negative: skipped)."""
-    T, H, d = k.shape
     if v.shape != k.shape:
         raise ValueError("k and v differ in shape")
-    ks, vs = _token_stride("k", k), _token_stride("v", v, T, k.dtype)
-    _need("slots", slots, torch.int32, (T,))
-    pages, _, ps = _kv4_cache(cache, H)
-    with _On(k, v, slots, cache, dev_status):
-        _check("diffattn_kv4_append", load().diffattn_kv4_append(
-            _ptr(k), ks, _ptr(v), vs, _dtype_code(k), _ptr(slots), T, H, d, _ptr(cache), pages,
-            ps, _ptr(dev_status), _stream(stream)))
+    dtype = _code("k", k)
+    ks, vs = _token_stride("k", k), _token_stride("v", v, None, k.dtype)
+    T, H, d = k.shape
+    _need("slots", slots, _I32, (T,))
+    pages, heads, ps = _kv4_cache(cache)
+    if heads != H:
+        raise ValueError("cache holds %d heads, k %d" % (heads, H))
+    at = _one_device(k, v, slots, cache, dev_status)
+    _run("diffattn_kv4_append", at, stream, k.data_ptr(), ks, v.data_ptr(), vs, dtype,
+         slots.data_ptr(), T, H, d, cache.data_ptr(), pages, ps, _ptr(dev_status))
     return cache
 
 
@@ -794,17 +821,19 @@ def diffattn_kv4_read(cache, slots, *, out=None, dtype=torch.bfloat16, dev_statu
     """Rows (k, v) [T, Hkv, 128] held at slots int32 [T].  Rows of negative
     slots are left as they were in `out` = (k, v), or are 0 in new tensors."""
     pages, H, ps = _kv4_cache(cache)
-    _need("slots", slots, torch.int32, (None,))
+    _need("slots", slots, _I32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [tokens]")
     T = slots.shape[0]
     if out is None:
         out = tuple(torch.zeros(T, H, 128, dtype=dtype, device=cache.device) for _ in "kv")
     k, v = out
+    code = _code("k", k)
     _need("k", k, k.dtype, (T, H, 128))
     _need("v", v, k.dtype, (T, H, 128))
-    with _On(cache, slots, k, v, dev_status):
-        _check("diffattn_kv4_read", load().diffattn_kv4_read(
-            _ptr(cache), pages, ps, _ptr(slots), T, H, 128, _ptr(k), _ptr(v), _dtype_code(k),
-            _ptr(dev_status), _stream(stream)))
+    at = _one_device(cache, slots, k, v, dev_status)
+    _run("diffattn_kv4_read", at, stream, cache.data_ptr(), pages, ps, slots.data_ptr(), T, H, 128,
+         k.data_ptr(), v.data_ptr(), code, _ptr(dev_status))
     return k, v
 
 
@@ -817,24 +846,33 @@ def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
     """V2 decode over the 4-bit cache.  q [B, Hq, 128] bf16; cache
     [n_pages, Hkv, page_size * 144] uint8; block_table int32 [B, max_pages];
     cache_lens int32 [B]; lam [Hq/2] fp32; out [B, Hq/2, 128]."""
-    dtype = _dtype_code(q)
+    code = _code("q", q)
     B, Hq, d = q.shape
     _need("q", q, q.dtype)
     pages, Hkv, ps = _kv4_cache(cache)
-    _need("block_table", block_table, torch.int32, (B, None))
-    _need("cache_lens", cache_lens, torch.int32, (B,))
-    _need("lam", lam, torch.float32, (Hq // 2,))
+    max_pages = _decode_lists(B, block_table, cache_lens, lam, Hq // 2)
+    at = _one_device(q, cache, block_table, cache_lens, lam, workspace, out, dev_status)
     if out is None:
-        out = torch.empty(B, Hq // 2, d, dtype=q.dtype, device=q.device)
-    _need("out", out, q.dtype, (B, Hq // 2, d))
-    with _On(q, cache, block_table, cache_lens, lam, workspace, out, dev_status) as on:
-        ws, ws_bytes = _workspace(workspace, diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv),
-                                  on.device, stream)
-        _check("diffattn_v2_decode_kv4", load().diffattn_v2_decode_kv4(
-            _ptr(q), _ptr(cache), pages, ps, _ptr(block_table), block_table.shape[1],
-            _ptr(cache_lens), int(window), _ptr(out), dtype, B, Hq, Hkv, d, _ptr(lam), _ptr(ws),
-            ws_bytes, _ptr(dev_status), _stream(stream)))
+        out = torch.empty((B, Hq // 2, d), dtype=q.dtype, device=q.device)
+    else:
+        _need("out", out, q.dtype, (B, Hq // 2, d))
+    ws = _workspace(workspace, 0 if workspace is not None else
+                    diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv), at, stream)
+    _run("diffattn_v2_decode_kv4", at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
+         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), window, out.data_ptr(), code, B,
+         Hq, Hkv, d, lam.data_ptr(), ws.data_ptr(), ws.nbytes, _ptr(dev_status))
     return out
+
+
+def _decode_lists(B, block_table, cache_lens, lam, n_lam):
+    """max_pages of a decode's tables, all checked."""
+    _need("block_table", block_table, _I32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_pages], not %s"
+                         % (B, tuple(block_table.shape)))
+    _need("cache_lens", cache_lens, _I32, (B,))
+    _need("lam", lam, _F32, (n_lam,))
+    return block_table.shape[1]
 
 
 def diffattn_v1_decode_kv4_workspace_size(batch, n_heads) -> int:
@@ -846,49 +884,51 @@ def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
                            out=None, dev_status=None, stream=None):
     """V1 decode over the 4-bit cache.  q [B, H, 128] bf16 (two 64-wide
     branches); cache [n_pages, H, page_size * 144] uint8; out [B, H, 128]."""
-    dtype = _dtype_code(q)
+    code = _code("q", q)
     B, H, d2 = q.shape
     _need("q", q, q.dtype)
-    pages, _, ps = _kv4_cache(cache, H)
-    _need("block_table", block_table, torch.int32, (B, None))
-    _need("cache_lens", cache_lens, torch.int32, (B,))
-    _need("lam", lam, torch.float32, (H,))
+    pages, heads, ps = _kv4_cache(cache)
+    if heads != H:
+        raise ValueError("cache holds %d heads, q %d" % (heads, H))
+    max_pages = _decode_lists(B, block_table, cache_lens, lam, H)
     if norm_weight is not None:
-        _need("norm_weight", norm_weight, torch.float32, (128,))
+        _need("norm_weight", norm_weight, _F32, (128,))
+    at = _one_device(q, cache, block_table, cache_lens, lam, norm_weight, workspace, out,
+                     dev_status)
     if out is None:
-        out = torch.empty(B, H, 128, dtype=q.dtype, device=q.device)
-    _need("out", out, q.dtype, (B, H, 128))
-    with _On(q, cache, block_table, cache_lens, lam, norm_weight, workspace, out,
-             dev_status) as on:
-        ws, ws_bytes = _workspace(workspace, diffattn_v1_decode_kv4_workspace_size(B, H),
-                                  on.device, stream)
-        _check("diffattn_v1_decode_kv4", load().diffattn_v1_decode_kv4(
-            _ptr(q), _ptr(cache), pages, ps, _ptr(block_table), block_table.shape[1],
-            _ptr(cache_lens), int(window), _ptr(out), dtype, B, H, d2 // 2, 128, _ptr(lam),
-            int(bool(apply_norm)), _ptr(norm_weight), float(norm_eps), float(lambda_init),
-            _ptr(ws), ws_bytes, _ptr(dev_status), _stream(stream)))
+        out = torch.empty((B, H, 128), dtype=q.dtype, device=q.device)
+    else:
+        _need("out", out, q.dtype, (B, H, 128))
+    ws = _workspace(workspace, 0 if workspace is not None else
+                    diffattn_v1_decode_kv4_workspace_size(B, H), at, stream)
+    _run("diffattn_v1_decode_kv4", at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
+         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), window, out.data_ptr(), code, B,
+         H, d2 // 2, 128, lam.data_ptr(), int(bool(apply_norm)), _ptr(norm_weight), norm_eps,
+         lambda_init, ws.data_ptr(), ws.nbytes, _ptr(dev_status))
     return out
 
 
 def _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight):
-    T, Hq, d = q.shape
+    code = _code("q", q)
     qs = _token_stride("q", q)
+    T, Hq, d = q.shape
     Hk, ks = 0, 0
     if k is not None:
         ks = _token_stride("k", k, T, q.dtype)
         Hk = k.shape[1]
         if k.shape[2] != d:
             raise ValueError("q and k differ in width")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need(name, w, torch.float32, (d,))
+    if q_weight is not None:
+        _need("q_weight", q_weight, _F32, (d,))
+    if k_weight is not None:
+        _need("k_weight", k_weight, _F32, (d,))
     rot = 0
     if inv_freq is not None:
-        _need("inv_freq", inv_freq, torch.float32, (None,))
-        rot = 2 * inv_freq.shape[0]
+        rot = 2 * inv_freq.numel()
+        _need("inv_freq", inv_freq, _F32, (rot // 2,))
     if positions is not None:
-        _need("positions", positions, torch.int32, (T,))
-    return T, Hq, Hk, d, qs, ks, rot
+        _need("positions", positions, _I32, (T,))
+    return code, T, Hq, Hk, d, qs, ks, rot
 
 
 def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
@@ -898,20 +938,25 @@ def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=
     (None: ones), then the rotation of the first 2 * len(inv_freq) features by
     positions int32 [T] * inv_freq fp32 (inv_freq None: no rotation).  k may
     be None.  Returns (q, k); `out` = (q, k) may be the arguments themselves."""
-    T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight)
+    code, T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight,
+                                                      k_weight)
+    ko, kos = None, 0
     if out is None:
-        out = (torch.empty(T, Hq, d, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(T, Hk, d, dtype=q.dtype, device=q.device))
-    qo, ko = out
-    if qo.shape != q.shape or (k is not None and ko.shape != k.shape):
-        raise ValueError("outputs must have the inputs' shapes")
-    qos = _token_stride("q out", qo, T, q.dtype)
-    kos = 0 if k is None else _token_stride("k out", ko, T, q.dtype)
-    with _On(q, k, positions, inv_freq, q_weight, k_weight, qo, ko):
-        _check("diffattn_qk_norm_rope", load().diffattn_qk_norm_rope(
-            _ptr(q), qs, _ptr(k), ks, _dtype_code(q), T, Hq, Hk, d, _ptr(q_weight),
-            _ptr(k_weight), float(norm_eps), _ptr(positions), _ptr(inv_freq), rot,
-            int(bool(interleaved)), _ptr(qo), qos, _ptr(ko), kos, _stream(stream)))
+        qo, qos = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device), Hq * d
+        if k is not None:
+            ko, kos = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device), Hk * d
+        at = _one_device(q, k, positions, inv_freq, q_weight, k_weight)
+    else:
+        qo, ko = out
+        if qo.shape != q.shape or (k is not None and ko.shape != k.shape):
+            raise ValueError("outputs must have the inputs' shapes")
+        qos = _token_stride("q out", qo, T, q.dtype)
+        if k is not None:
+            kos = _token_stride("k out", ko, T, q.dtype)
+        at = _one_device(q, k, positions, inv_freq, q_weight, k_weight, qo, ko)
+    _run("diffattn_qk_norm_rope", at, stream, q.data_ptr(), qs, _ptr(k), ks, code, T, Hq, Hk, d,
+         _ptr(q_weight), _ptr(k_weight), norm_eps, _ptr(positions), _ptr(inv_freq), rot,
+         int(bool(interleaved)), qo.data_ptr(), qos, _ptr(ko), kos)
     return qo, ko
 
 
@@ -926,24 +971,26 @@ def diffattn_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, *, q_we
     """Gradients of diffattn_qk_norm_rope: q, k are its inputs, dq_out, dk_out
     (fp32) the gradients of its outputs.  Returns a dict of fp32 tensors: dq,
     dk, dq_weight, dk_weight (None where the input is None)."""
-    T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight)
-    f32 = dict(dtype=torch.float32, device=q.device)
+    code, T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight,
+                                                      k_weight)
     if dq_out.shape != q.shape or (k is not None and dk_out.shape != k.shape):
         raise ValueError("the gradients must have the inputs' shapes")
-    gqs = _token_stride("dq_out", dq_out, T, torch.float32)
-    gks = 0 if k is None else _token_stride("dk_out", dk_out, T, torch.float32)
-    r = {"dq": torch.empty(T, Hq, d, **f32),
-         "dk": None if k is None else torch.empty(T, Hk, d, **f32),
-         "dq_weight": None if q_weight is None else torch.empty(d, **f32),
-         "dk_weight": None if k is None or k_weight is None else torch.empty(d, **f32)}
-    with _On(q, k, dq_out, dk_out, positions, inv_freq, q_weight, k_weight, workspace) as on:
-        ws, ws_bytes = _workspace(
-            workspace, diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), on.device, stream)
-        _check("diffattn_qk_norm_rope_bwd", load().diffattn_qk_norm_rope_bwd(
-            _ptr(q), qs, _ptr(k), ks, _dtype_code(q), _ptr(dq_out), gqs, _ptr(dk_out), gks, T, Hq,
-            Hk, d, _ptr(q_weight), _ptr(k_weight), float(norm_eps), _ptr(positions),
-            _ptr(inv_freq), rot, int(bool(interleaved)), _ptr(r["dq"]), _ptr(r["dk"]),
-            _ptr(r["dq_weight"]), _ptr(r["dk_weight"]), _ptr(ws), ws_bytes, _stream(stream)))
+    gqs = _token_stride("dq_out", dq_out, T, _F32)
+    gks = 0 if k is None else _token_stride("dk_out", dk_out, T, _F32)
+    at = _one_device(q, k, dq_out, dk_out, positions, inv_freq, q_weight, k_weight, workspace)
+    dev = q.device
+    r = {"dq": torch.empty((T, Hq, d), dtype=_F32, device=dev),
+         "dk": None if k is None else torch.empty((T, Hk, d), dtype=_F32, device=dev),
+         "dq_weight": None if q_weight is None else torch.empty(d, dtype=_F32, device=dev),
+         "dk_weight": None if k is None or k_weight is None else
+         torch.empty(d, dtype=_F32, device=dev)}
+    ws = _workspace(workspace, 0 if workspace is not None else
+                    diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), at, stream)
+    _run("diffattn_qk_norm_rope_bwd", at, stream, q.data_ptr(), qs, _ptr(k), ks, code,
+         dq_out.data_ptr(), gqs, _ptr(dk_out), gks, T, Hq, Hk, d, _ptr(q_weight), _ptr(k_weight),
+         norm_eps, _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
+         r["dq"].data_ptr(), _ptr(r["dk"]), _ptr(r["dq_weight"]), _ptr(r["dk_weight"]),
+         ws.data_ptr(), ws.nbytes)
     return r
 
 

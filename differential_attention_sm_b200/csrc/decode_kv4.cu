@@ -54,6 +54,8 @@ constexpr int kPlanSms = 148;      // fixed: the workspace size is the same on e
 constexpr int kMinStages = 2;      // shortest run of a warp
 constexpr int kChunkHeads = 16;    // query heads that share one pass over the cache
 constexpr float kNoMax = -3.0e38f;
+constexpr uint32_t kNoTile = 0xFFFFFFFFu;   // of no use to the segment
+constexpr uint32_t kBadTile = 0xFFFFFFFEu;  // on a page out of range
 constexpr float kShift = 5.0f;    // p = 2^(s - m + kShift)
 constexpr float kRaise = 10.0f;   // m is raised when a score passes m + kRaise
 
@@ -138,6 +140,33 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 P, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_to(uint32_t dst, const void* src, uint32_t bytes,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // Scale byte `i` of w in both halves; scale bytes `i`, `i + 1` in the halves.
 template <int i>
 __device__ __forceinline__ uint32_t scale_twice(uint32_t w) {
@@ -153,6 +182,7 @@ template <int NT>
 struct WarpState {
   float o[NT][8][4];  // channels 16 * (lane / 4) + 2 * i, + 1; columns 2 * (lane % 4), + 1
   float l[NT][2], m[NT][2];
+  float top[NT][2];  // the unscaled score above which m is raised
 };
 
 // Sixteen tokens' scores: c[nt] holds tokens g, g + 8 of columns 2q, 2q + 1.
@@ -225,8 +255,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
   const uint32_t lane = threadIdx.x & 31u;
   const int warp = (int)(threadIdx.x >> 5);
   const uint32_t g = lane >> 2, qd = lane & 3u;
-  uint8_t* ring = smem + warp * kRing * kStageBytes;
+  const uint32_t ring_at = smem_u32(smem) + warp * kRing * kStageBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * kRing * kStageBytes) + warp * kRing;
+  const uint32_t bars_at = smem_u32(bars);
   uint32_t* loaded = reinterpret_cast<uint32_t*>(smem + kWarps * kRing * (kStageBytes + 8)) +
                      warp * kRing;  // which tiles of a ring slot hold tokens
   if (lane == 0) {
@@ -235,7 +266,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
     fence_proxy_async_smem();
   }
   __syncwarp();
-  const uint32_t ring_at = smem_u32(ring);
 
   const int units = a.heads * a.chunks;  // of one sequence
   const long long total = stages_before(a, a.batch) * units;
@@ -270,7 +300,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
 
   int slot = 0;          // next ring slot
   uint32_t parity = 0;   // of that slot
-  bool failed = false;
   while (pos < end) {
     const int unit = (int)((pos - base) / n_b);
     const int s_first = (int)((pos - base) - (long long)unit * n_b);
@@ -314,7 +343,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         qf[n][i] = pack_f16(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
-      const float up = __uint_as_float(e << 23) * a.scale;
+      // Positive, so that it can multiply a masked score's infinity; scores
+      // that this floor touches are 0 to any precision here.
+      const float up = fmaxf(__uint_as_float(e << 23) * a.scale, 1.0e-30f);
       back[n][0] = __shfl_sync(0xffffffffu, up, 8 * qd);
       back[n][1] = __shfl_sync(0xffffffffu, up, 8 * qd + 4);
     }
@@ -328,42 +359,41 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
         for (int j = 0; j < 4; ++j) w.o[n][i][j] = 0.f;
       w.l[n][0] = w.l[n][1] = 0.f;
       w.m[n][0] = w.m[n][1] = kNoMax;
+      w.top[n][0] = w.top[n][1] = kNoMax;
     }
 
-    // Pages of 32 stages at a time, one stage per lane, the next 32 ahead.
+    // Tiles of 32 stages at a time, one stage per lane, the next 32 ahead.
     const int* row = a.table + (size_t)b * a.max_pages;
     const int first_tile = lo >> 4, last_tile = (len - 1) >> 4;
-    auto page_of = [&](int i, int half) {  // page of a tile of stage s0 + i; -1: not needed
+    const int sh = a.page_shift - 4;
+    auto tile_of = [&](int i, int half) -> uint32_t {  // index in the cache
       const int tile = 2 * (s0 + i) + half;
-      return i < count && tile >= first_tile && tile <= last_tile
-                 ? row[tile >> (a.page_shift - 4)] : -1;
+      if (i >= count || tile < first_tile || tile > last_tile) return kNoTile;
+      const int page = row[tile >> sh];
+      if ((unsigned)page >= (unsigned)a.n_pages) return kBadTile;
+      return ((((uint32_t)page * (uint32_t)a.heads + (uint32_t)kvh) << sh) +
+              (uint32_t)(tile & ((1 << sh) - 1)));
     };
-    int pa = page_of((int)lane, 0), pb = page_of((int)lane, 1);
-    int na = page_of(32 + (int)lane, 0), nb = page_of(32 + (int)lane, 1);
-    const int64_t head_tiles = 1 << (a.page_shift - 4);
+    uint32_t ta = tile_of((int)lane, 0), tb = tile_of((int)lane, 1);
+    uint32_t na = tile_of(32 + (int)lane, 0), nb = tile_of(32 + (int)lane, 1);
     auto issue = [&](int i, int to) {  // stage i of the segment into ring slot `to`
-      const int ga = __shfl_sync(0xffffffffu, pa, i & 31), gb = __shfl_sync(0xffffffffu, pb, i & 31);
+      const uint32_t ga = __shfl_sync(0xffffffffu, ta, i & 31),
+                     gb = __shfl_sync(0xffffffffu, tb, i & 31);
       if (lane == 0) {
-        const int tile = 2 * (s0 + i);
-        const bool in_a = tile >= first_tile && tile <= last_tile;
-        const bool in_b = tile + 1 >= first_tile && tile + 1 <= last_tile;
-        const bool ok_a = in_a && (unsigned)ga < (unsigned)a.n_pages;
-        const bool ok_b = in_b && (unsigned)gb < (unsigned)a.n_pages;
-        if (in_a != ok_a || in_b != ok_b) report(a.dev_status, DA_ERR_PAGE);
-        loaded[to] = (ok_a ? 1u : 0u) | (ok_b ? 2u : 0u);
-        uint8_t* dst = ring + to * kStageBytes;
-        const int mask = (int)head_tiles - 1;
-        const uint8_t* src_a =
-            a.cache + (((int64_t)ga * a.heads + kvh) * head_tiles + (tile & mask)) * kKv4TileBytes;
-        const uint8_t* src_b =
-            a.cache +
-            (((int64_t)gb * a.heads + kvh) * head_tiles + ((tile + 1) & mask)) * kKv4TileBytes;
-        mbar_arrive_expect_tx(&bars[to], (ok_a ? kKv4TileBytes : 0) + (ok_b ? kKv4TileBytes : 0));
-        if (ok_a && ok_b && src_b == src_a + kKv4TileBytes) {
-          bulk_load(dst, src_a, kStageBytes, &bars[to]);
+        const uint32_t dst = ring_at + to * kStageBytes, bar = bars_at + to * 8;
+        if (gb == ga + 1u && gb < kBadTile) {
+          loaded[to] = 3u;
+          expect(bar, kStageBytes);
+          bulk_to(dst, a.cache + (uint64_t)ga * kKv4TileBytes, kStageBytes, bar);
         } else {
-          if (ok_a) bulk_load(dst, src_a, kKv4TileBytes, &bars[to]);
-          if (ok_b) bulk_load(dst + kKv4TileBytes, src_b, kKv4TileBytes, &bars[to]);
+          if (ga == kBadTile || gb == kBadTile) report(a.dev_status, DA_ERR_PAGE);
+          const bool ok_a = ga < kBadTile, ok_b = gb < kBadTile;
+          loaded[to] = (ok_a ? 1u : 0u) | (ok_b ? 2u : 0u);
+          expect(bar, (ok_a ? kKv4TileBytes : 0) + (ok_b ? kKv4TileBytes : 0));
+          if (ok_a) bulk_to(dst, a.cache + (uint64_t)ga * kKv4TileBytes, kKv4TileBytes, bar);
+          if (ok_b)
+            bulk_to(dst + kKv4TileBytes, a.cache + (uint64_t)gb * kKv4TileBytes, kKv4TileBytes,
+                    bar);
         }
       }
     };
@@ -374,15 +404,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
     }
 
     for (int i = 0; i < count; ++i) {
-      mbar_wait(&bars[slot], parity, a.dev_status, &failed);
-      if (__any_sync(0xffffffffu, failed)) {
-        // Leave no copy of ours in flight: wait for the other slots, bounded too.
-        for (int k = i + 1; k < issued; ++k) {
-          if (++slot == kRing) slot = 0, parity ^= 1u;
-          failed = false;
-          mbar_wait(&bars[slot], parity, a.dev_status, &failed);
+      if (!__all_sync(0xffffffffu, try_wait(bars_at + slot * 8, parity))) {
+        bool failed = false;
+        mbar_wait(&bars[slot], parity, a.dev_status, &failed);
+        if (__any_sync(0xffffffffu, failed)) {
+          // Leave no copy of ours in flight: wait for the other slots, bounded too.
+          for (int k = i + 1; k < issued; ++k) {
+            if (++slot == kRing) slot = 0, parity ^= 1u;
+            failed = false;
+            mbar_wait(&bars[slot], parity, a.dev_status, &failed);
+          }
+          return;
         }
-        return;
       }
       const uint32_t at = ring_at + slot * kStageBytes;
       const uint32_t have = loaded[slot];
@@ -390,17 +423,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
       tile_scores<NT>(at, lane, qf, c[0]);
       tile_scores<NT>(at + kKv4TileBytes, lane, qf, c[1]);
       const int t0 = (s0 + i) * kStageTokens;
-      const bool whole = have == 3u && t0 >= lo && t0 + kStageTokens <= len;
-      float mx[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[t][n][j] *= back[n][j & 1];
-      }
       uint32_t seen[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
-      if (!whole) {
+      if (have != 3u || t0 < lo || t0 + kStageTokens > len) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const bool there = (have >> t) & 1u;
@@ -420,13 +444,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
                          (sees(2 * (int)qd + 8 * h + 1) ? 0xFFFF0000u : 0u);
         }
       }
+      float mx[NT][2];
       bool raise = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          mx[n][j] = max3(fmaxf(c[0][n][j], c[0][n][j + 2]), c[1][n][j], c[1][n][j + 2]);
-          raise |= mx[n][j] > w.m[n][j] + kRaise;
+          mx[n][j] = fmaxf(max3(c[0][n][j], c[0][n][j + 2], c[1][n][j]), c[1][n][j + 2]);
+          raise |= mx[n][j] > w.top[n][j];
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -437,9 +462,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, w.m[n][j]);
+            top = fmaxf(top * back[n][j], w.m[n][j]);
             const float f = ex2(w.m[n][j] - top);
             w.m[n][j] = top;
+            w.top[n][j] = top > kNoMax ? (top + kRaise) / back[n][j] : kNoMax;
             w.l[n][j] *= f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) w.o[n][k][j] *= f, w.o[n][k][j + 2] *= f;
@@ -450,9 +476,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
         uint32_t p[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float m0 = w.m[n][0] - kShift, m1 = w.m[n][1] - kShift;
-          const float p0 = ex2(c[t][n][0] - m0), p1 = ex2(c[t][n][1] - m1);
-          const float p2 = ex2(c[t][n][2] - m0), p3 = ex2(c[t][n][3] - m1);
+          const float m0 = kShift - w.m[n][0], m1 = kShift - w.m[n][1];
+          const float p0 = ex2(fmaf(c[t][n][0], back[n][0], m0)),
+                      p1 = ex2(fmaf(c[t][n][1], back[n][1], m1)),
+                      p2 = ex2(fmaf(c[t][n][2], back[n][0], m0)),
+                      p3 = ex2(fmaf(c[t][n][3], back[n][1], m1));
           w.l[n][0] += p0 + p2;
           w.l[n][1] += p1 + p3;
           p[n][0] = movmatrix_trans(pack_f16(p0, p1));
@@ -464,13 +492,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
       if (issued < count) {
         issue(issued, slot);
         if ((++issued & 31) == 0) {
-          pa = na, pb = nb;
-          na = page_of(issued + 32 + (int)lane, 0);
-          nb = page_of(issued + 32 + (int)lane, 1);
+          ta = na, tb = nb;
+          na = tile_of(issued + 32 + (int)lane, 0);
+          nb = tile_of(issued + 32 + (int)lane, 1);
         }
       }
       if (++slot == kRing) slot = 0, parity ^= 1u;
     }
+
     // The segment's sums.  Slots are ordered as the segments are: the next
     // segment has the next unit or the next run.
     const long long part = (long long)b * units + unit + me;
@@ -630,7 +659,8 @@ int check(const void* q, const void* cache, const int* table, const int* lens, c
     return DA_ERR_INVALID_ARG;
   if (dtype != DA_BF16 || !kv4_page_size_ok(page_size)) return DA_ERR_UNSUPPORTED;
   if ((long long)n_pages * page_size >= (1LL << 31) ||
-      (long long)max_pages * page_size >= (1LL << 31))
+      (long long)max_pages * page_size >= (1LL << 31) ||
+      (long long)n_pages * page_size / kKv4Tile * heads >= (long long)kBadTile)
     return DA_ERR_UNSUPPORTED;
   return DA_OK;
 }

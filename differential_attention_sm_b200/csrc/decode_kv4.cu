@@ -7,7 +7,7 @@
 //
 // Bound by the cache's bytes: 144 per token and KV head, and close behind by
 // the instructions that turn codes into operands.  So:
-//  - The work is one line of stages (32 tokens of one KV head of one
+//  - The work is one line of stages (64 tokens of one KV head of one
 //    sequence), computed from the lengths on the device and cut into equal
 //    runs, one for each warp of the grid: no lengths on the host, no idle
 //    warps behind ragged lengths, no synchronisation between warps.
@@ -44,14 +44,14 @@ namespace da {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kStageTokens = 32;
-constexpr int kStageBytes = 2 * kKv4TileBytes;
+constexpr int kTiles = 4;  // of a stage
+constexpr int kStageTokens = kTiles * kKv4Tile;
+constexpr int kStageBytes = kTiles * kKv4TileBytes;
 constexpr int kWarps = 4;
-constexpr int kRing = 3;
-constexpr int kCtasPerSm = 4;
-constexpr int kCtasPerSmWide = 3;  // two column tiles need more registers
+constexpr int kRing = 2;
+constexpr int kCtasPerSm = 3;
 constexpr int kPlanSms = 148;      // fixed: the workspace size is the same on every device
-constexpr int kMinStages = 2;      // shortest run of a warp
+constexpr int kMinStages = 1;      // shortest run of a warp
 constexpr int kChunkHeads = 16;    // query heads that share one pass over the cache
 constexpr float kNoMax = -3.0e38f;
 constexpr uint32_t kNoTile = 0xFFFFFFFFu;   // of no use to the segment
@@ -94,24 +94,54 @@ __device__ __forceinline__ int stages_of(const Kv4Args& a, int b) {
   return len > lo ? (len - 1) / kStageTokens - lo / kStageTokens + 1 : 0;
 }
 
-// Stages of one (KV head, pass) of the sequences before `upto` (all of them
-// when it is the batch); the whole warp calls it.
-__device__ __forceinline__ long long stages_before(const Kv4Args& a, int upto) {
-  long long n = 0;
-  for (int b = (int)lane_id(); b < upto; b += 32) n += stages_of(a, b);
+// Stages of one (KV head, pass) of the sequences before b, and of all; the
+// whole warp calls it.
+__device__ __forceinline__ void stage_sums(const Kv4Args& a, int b, long long& before,
+                                           long long& total) {
+  before = total = 0;
+  for (int i = (int)lane_id(); i < a.batch; i += 32) {
+    const int n = stages_of(a, i);
+    total += n;
+    if (i < b) before += n;
+  }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-  return n;
+  for (int off = 16; off; off >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+    total += __shfl_xor_sync(0xffffffffu, total, off);
+  }
+}
+
+// x / y for x >= 0, y > 0; nearly always of 32 bits, where it costs a fifth.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (long long)((uint32_t)x / (uint32_t)y);
+  return x / y;
 }
 
 __device__ __forceinline__ long long run_length(const Kv4Args& a, long long total) {
-  const long long q = (total + a.runs - 1) / a.runs;
+  const long long q = divide(total + a.runs - 1, a.runs);
   return q < kMinStages ? kMinStages : q;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// Both halves of x times the low (high) half of y.
+__device__ __forceinline__ uint32_t hmul2_lo(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 d;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 d, {l, l};\n\t"
+      "mul.f16x2 %0, %1, d;\n\t}"
+      : "=r"(r)
+      : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2_hi(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 d;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 d, {h, h};\n\t"
+      "mul.f16x2 %0, %1, d;\n\t}"
+      : "=r"(r)
+      : "r"(x), "r"(y));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -126,6 +156,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
@@ -167,11 +206,7 @@ __device__ __forceinline__ void bulk_to(uint32_t dst, const void* src, uint32_t 
       : "memory");
 }
 
-// Scale byte `i` of w in both halves; scale bytes `i`, `i + 1` in the halves.
-template <int i>
-__device__ __forceinline__ uint32_t scale_twice(uint32_t w) {
-  return __byte_perm(w, 0u, 0x0404u | (i << 4) | (i << 12)) >> 1;
-}
+// Scale bytes `i`, `i + 1` of w in the halves.
 template <int i>
 __device__ __forceinline__ uint32_t scale_pair(uint32_t w) {
   return __byte_perm(w, 0u, 0x0404u | (i << 4) | ((i + 1) << 12)) >> 1;
@@ -182,35 +217,51 @@ template <int NT>
 struct WarpState {
   float o[NT][8][4];  // channels 16 * (lane / 4) + 2 * i, + 1; columns 2 * (lane % 4), + 1
   float l[NT][2], m[NT][2];
+  float off[NT][2];  // kShift - m
   float top[NT][2];  // the unscaled score above which m is raised
 };
 
-// Sixteen tokens' scores: c[nt] holds tokens g, g + 8 of columns 2q, 2q + 1.
+// The scores of two tiles: c[t][n] holds tokens g, g + 8 of tile t, columns 2q,
+// 2q + 1.  The tiles are taken turn and turn about, so that neither waits for
+// its own last product.
 template <int NT>
-__device__ __forceinline__ void tile_scores(uint32_t at, uint32_t lane, const uint32_t (&qf)[NT][16],
-                                            float (&c)[NT][4]) {
-  const uint4 k0 = lds128(at + lane * 16), k1 = lds128(at + 512 + lane * 16);
-  const uint32_t sw = lds32(at + kKv4KScales + lane * 4);
-  const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-  const uint32_t s00 = scale_twice<0>(sw), s01 = scale_twice<1>(sw), s10 = scale_twice<2>(sw),
-                 s11 = scale_twice<3>(sw);
+__device__ __forceinline__ void pair_scores(uint32_t at, uint32_t lane,
+                                            const uint32_t (&qf)[NT][16], float (&c)[2][NT][4]) {
+  uint32_t w0[2][4], w1[2][4], s[2][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+  for (int t = 0; t < 2; ++t) {
+    const uint4 k0 = lds128(at + t * kKv4TileBytes + lane * 16),
+                k1 = lds128(at + t * kKv4TileBytes + 512 + lane * 16);
+    const uint32_t sw = lds32(at + t * kKv4TileBytes + kKv4KScales + lane * 4);
+    w0[t][0] = k0.x, w0[t][1] = k0.y, w0[t][2] = k0.z, w0[t][3] = k0.w;
+    w1[t][0] = k1.x, w1[t][1] = k1.y, w1[t][2] = k1.z, w1[t][3] = k1.w;
+    // Tokens (g, g + 8) of the lane's even and of its odd block.
+    s[t][0] = (sw << 7) & 0x7F807F80u;
+    s[t][1] = (sw >> 1) & 0x7F807F80u;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t s0 = i < 2 ? s00 : s01, s1 = i < 2 ? s10 : s11;
-    uint32_t a[4], b[4];
-    e2m1x8_to_f16x2(w0[i], a[0], a[1], a[2], a[3]);
-    e2m1x8_to_f16x2(w1[i], b[0], b[1], b[2], b[3]);
+    uint32_t a[2][4], b[2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] = hmul2(a[j], s0), b[j] = hmul2(b[j], s1);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mma_f16(c[n], a[0], b[0], a[1], b[1], qf[n][4 * i], qf[n][4 * i + 1]);
-      mma_f16(c[n], a[2], b[2], a[3], b[3], qf[n][4 * i + 2], qf[n][4 * i + 3]);
+    for (int t = 0; t < 2; ++t) {
+      e2m1x8_to_f16x2(w0[t][i], a[t][0], a[t][1], a[t][2], a[t][3]);
+      e2m1x8_to_f16x2(w1[t][i], b[t][0], b[t][1], b[t][2], b[t][3]);
     }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t sc = s[t][i / 2];
+        const uint32_t x0 = hmul2_lo(a[t][j], sc), x1 = hmul2_hi(b[t][j], sc);
+        const uint32_t x2 = hmul2_lo(a[t][j + 1], sc), x3 = hmul2_hi(b[t][j + 1], sc);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (i == 0 && j == 0)
+            mma_f16_first(c[t][n], x0, x1, x2, x3, qf[n][0], qf[n][1]);
+          else
+            mma_f16(c[t][n], x0, x1, x2, x3, qf[n][4 * i + j], qf[n][4 * i + j + 1]);
+        }
+      }
   }
 }
 
@@ -248,7 +299,7 @@ __device__ __forceinline__ void tile_values(uint32_t at, uint32_t lane, uint32_t
 }
 
 template <int NT, bool kV1>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSmWide)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     kv4_decode_kernel(const Kv4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -268,7 +319,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
   __syncwarp();
 
   const int units = a.heads * a.chunks;  // of one sequence
-  const long long total = stages_before(a, a.batch) * units;
+  long long before, total;
+  stage_sums(a, 0, before, total);
+  total *= units;
   const long long run = run_length(a, total);
   // Neighbouring runs lie on different SMs.
   const int me = warp * (int)gridDim.x + (int)blockIdx.x;
@@ -301,13 +354,63 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
   int slot = 0;          // next ring slot
   uint32_t parity = 0;   // of that slot
   while (pos < end) {
-    const int unit = (int)((pos - base) / n_b);
+    const int unit = (int)divide(pos - base, n_b);
     const int s_first = (int)((pos - base) - (long long)unit * n_b);
     const int count = (int)(end - pos < n_b - s_first ? end - pos : n_b - s_first);
     const int kvh = unit / a.chunks, chunk = unit - kvh * a.chunks;
     int lo, len;
     span_of(a, b, lo, len);
     const int s0 = lo / kStageTokens + s_first;  // absolute stage
+
+    // The next 32 tiles (8 stages) of the segment, one per lane, and the 32
+    // behind them.
+    const int* row = a.table + (size_t)b * a.max_pages;
+    const int first_tile = lo >> 4, last_tile = min((len - 1) >> 4, kTiles * (s0 + count) - 1);
+    const int sh = a.page_shift - 4;
+    auto tile_of = [&](int at) -> uint32_t {  // index in the cache of the segment's tile `at`
+      const int t = kTiles * s0 + at;
+      if (t < first_tile || t > last_tile) return kNoTile;
+      const int page = row[t >> sh];
+      if ((unsigned)page >= (unsigned)a.n_pages) return kBadTile;
+      return (((uint32_t)page * (uint32_t)a.heads + (uint32_t)kvh) << sh) +
+             (uint32_t)(t & ((1 << sh) - 1));
+    };
+    // Bit l: the tiles of lanes l and l + 1 are neighbours in memory.
+    auto joined = [&](uint32_t mine) {
+      const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+      return __ballot_sync(0xffffffffu, next == mine + 1u && next < kBadTile);
+    };
+    uint32_t tile = tile_of((int)lane), ahead = tile_of(32 + (int)lane);
+    uint32_t join = joined(tile);
+    auto issue = [&](int i, int to) {  // stage i of the segment into ring slot `to`
+      const uint32_t lead = (uint32_t)(i & 7) * kTiles;
+      const uint32_t dst = ring_at + to * kStageBytes, bar = bars_at + to * 8;
+      if (((join >> lead) & 7u) == 7u) {
+        if (lane == lead) {
+          loaded[to] = 15u;
+          expect(bar, kStageBytes);
+          bulk_to(dst, a.cache + (uint64_t)tile * kKv4TileBytes, kStageBytes, bar);
+        }
+      } else {
+        const bool mine = lane - lead < (uint32_t)kTiles;
+        const bool ok = mine && tile < kBadTile;
+        const uint32_t have = __ballot_sync(0xffffffffu, ok) >> lead;
+        if (mine && tile == kBadTile) report(a.dev_status, DA_ERR_PAGE);
+        if (lane == lead) {
+          loaded[to] = have;
+          expect(bar, __popc(have) * kKv4TileBytes);
+        }
+        __syncwarp();
+        if (ok)
+          bulk_to(dst + (lane - lead) * kKv4TileBytes, a.cache + (uint64_t)tile * kKv4TileBytes,
+                  kKv4TileBytes, bar);
+      }
+    };
+    int issued = 0;
+    for (int to = slot; issued < kRing && issued < count; ++issued) {
+      issue(issued, to);
+      if (++to == kRing) to = 0;
+    }
 
     // Query fragments: column g of tile n, channels 32 * qd ...
     uint32_t qf[NT][16];
@@ -359,48 +462,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
         for (int j = 0; j < 4; ++j) w.o[n][i][j] = 0.f;
       w.l[n][0] = w.l[n][1] = 0.f;
       w.m[n][0] = w.m[n][1] = kNoMax;
+      w.off[n][0] = w.off[n][1] = kShift - kNoMax;
       w.top[n][0] = w.top[n][1] = kNoMax;
-    }
-
-    // Tiles of 32 stages at a time, one stage per lane, the next 32 ahead.
-    const int* row = a.table + (size_t)b * a.max_pages;
-    const int first_tile = lo >> 4, last_tile = (len - 1) >> 4;
-    const int sh = a.page_shift - 4;
-    auto tile_of = [&](int i, int half) -> uint32_t {  // index in the cache
-      const int tile = 2 * (s0 + i) + half;
-      if (i >= count || tile < first_tile || tile > last_tile) return kNoTile;
-      const int page = row[tile >> sh];
-      if ((unsigned)page >= (unsigned)a.n_pages) return kBadTile;
-      return ((((uint32_t)page * (uint32_t)a.heads + (uint32_t)kvh) << sh) +
-              (uint32_t)(tile & ((1 << sh) - 1)));
-    };
-    uint32_t ta = tile_of((int)lane, 0), tb = tile_of((int)lane, 1);
-    uint32_t na = tile_of(32 + (int)lane, 0), nb = tile_of(32 + (int)lane, 1);
-    auto issue = [&](int i, int to) {  // stage i of the segment into ring slot `to`
-      const uint32_t ga = __shfl_sync(0xffffffffu, ta, i & 31),
-                     gb = __shfl_sync(0xffffffffu, tb, i & 31);
-      if (lane == 0) {
-        const uint32_t dst = ring_at + to * kStageBytes, bar = bars_at + to * 8;
-        if (gb == ga + 1u && gb < kBadTile) {
-          loaded[to] = 3u;
-          expect(bar, kStageBytes);
-          bulk_to(dst, a.cache + (uint64_t)ga * kKv4TileBytes, kStageBytes, bar);
-        } else {
-          if (ga == kBadTile || gb == kBadTile) report(a.dev_status, DA_ERR_PAGE);
-          const bool ok_a = ga < kBadTile, ok_b = gb < kBadTile;
-          loaded[to] = (ok_a ? 1u : 0u) | (ok_b ? 2u : 0u);
-          expect(bar, (ok_a ? kKv4TileBytes : 0) + (ok_b ? kKv4TileBytes : 0));
-          if (ok_a) bulk_to(dst, a.cache + (uint64_t)ga * kKv4TileBytes, kKv4TileBytes, bar);
-          if (ok_b)
-            bulk_to(dst + kKv4TileBytes, a.cache + (uint64_t)gb * kKv4TileBytes, kKv4TileBytes,
-                    bar);
-        }
-      }
-    };
-    int issued = 0, to = slot;
-    for (; issued < kRing && issued < count; ++issued) {
-      issue(issued, to);
-      if (++to == kRing) to = 0;
     }
 
     for (int i = 0; i < count; ++i) {
@@ -417,85 +480,89 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
           return;
         }
       }
-      const uint32_t at = ring_at + slot * kStageBytes;
       const uint32_t have = loaded[slot];
-      float c[2][NT][4];
-      tile_scores<NT>(at, lane, qf, c[0]);
-      tile_scores<NT>(at + kKv4TileBytes, lane, qf, c[1]);
-      const int t0 = (s0 + i) * kStageTokens;
-      uint32_t seen[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
-      if (have != 3u || t0 < lo || t0 + kStageTokens > len) {
+      const int first_tok = (s0 + i) * kStageTokens;
+      const bool part = have != 15u || first_tok < lo || first_tok + kStageTokens > len;
+#pragma unroll 1
+      for (int pair = 0; pair < kTiles / 2; ++pair) {
+        const uint32_t at = ring_at + slot * kStageBytes + pair * 2 * kKv4TileBytes;
+        float c[2][NT][4];
+        pair_scores<NT>(at, lane, qf, c);
+        uint32_t seen[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+        if (part) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const bool there = (have >> t) & 1u;
-          auto sees = [&](int u) {
-            const int tok = t0 + 16 * t + u;
-            return there && tok >= lo && tok < len;
-          };
-          const bool r0 = sees((int)g), r1 = sees((int)g + 8);
+          for (int t = 0; t < 2; ++t) {
+            const bool there = (have >> (2 * pair + t)) & 1u;
+            auto sees = [&](int u) {
+              const int tok = first_tok + 32 * pair + 16 * t + u;
+              return there && tok >= lo && tok < len;
+            };
+            const bool r0 = sees((int)g), r1 = sees((int)g + 8);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (!r0) c[t][n][0] = c[t][n][1] = -INFINITY;
-            if (!r1) c[t][n][2] = c[t][n][3] = -INFINITY;
+            for (int n = 0; n < NT; ++n) {
+              if (!r0) c[t][n][0] = c[t][n][1] = -INFINITY;
+              if (!r1) c[t][n][2] = c[t][n][3] = -INFINITY;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              seen[t][h] = (sees(2 * (int)qd + 8 * h) ? 0xFFFFu : 0u) |
+                           (sees(2 * (int)qd + 8 * h + 1) ? 0xFFFF0000u : 0u);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            seen[t][h] = (sees(2 * (int)qd + 8 * h) ? 0xFFFFu : 0u) |
-                         (sees(2 * (int)qd + 8 * h + 1) ? 0xFFFF0000u : 0u);
         }
-      }
-      float mx[NT][2];
-      bool raise = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mx[n][j] = fmaxf(max3(c[0][n][j], c[0][n][j + 2], c[1][n][j]), c[1][n][j + 2]);
-          raise |= mx[n][j] > w.top[n][j];
-        }
-      if (__any_sync(0xffffffffu, raise)) {
+        float mx[NT][2];
+        bool raise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = mx[n][j];
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top * back[n][j], w.m[n][j]);
-            const float f = ex2(w.m[n][j] - top);
-            w.m[n][j] = top;
-            w.top[n][j] = top > kNoMax ? (top + kRaise) / back[n][j] : kNoMax;
-            w.l[n][j] *= f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w.o[n][k][j] *= f, w.o[n][k][j + 2] *= f;
+            mx[n][j] = fmaxf(max3(c[0][n][j], c[0][n][j + 2], c[1][n][j]), c[1][n][j + 2]);
+            raise |= mx[n][j] > w.top[n][j];
           }
-      }
+        if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        uint32_t p[NT][2];
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float m0 = kShift - w.m[n][0], m1 = kShift - w.m[n][1];
-          const float p0 = ex2(fmaf(c[t][n][0], back[n][0], m0)),
-                      p1 = ex2(fmaf(c[t][n][1], back[n][1], m1)),
-                      p2 = ex2(fmaf(c[t][n][2], back[n][0], m0)),
-                      p3 = ex2(fmaf(c[t][n][3], back[n][1], m1));
-          w.l[n][0] += p0 + p2;
-          w.l[n][1] += p1 + p3;
-          p[n][0] = movmatrix_trans(pack_f16(p0, p1));
-          p[n][1] = movmatrix_trans(pack_f16(p2, p3));
+            for (int j = 0; j < 2; ++j) {
+              float top = mx[n][j];
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              top = fmaxf(top * back[n][j], w.m[n][j]);
+              const float f = ex2(w.m[n][j] - top);
+              w.m[n][j] = top;
+              w.off[n][j] = kShift - top;
+              w.top[n][j] = top > kNoMax ? (top + kRaise) / back[n][j] : kNoMax;
+              w.l[n][j] *= f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w.o[n][k][j] *= f, w.o[n][k][j + 2] *= f;
+            }
         }
-        tile_values<NT>(at + t * kKv4TileBytes, lane, seen[t][0], seen[t][1], p, w.o);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint32_t p[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float p0 = ex2(fmaf(c[t][n][0], back[n][0], w.off[n][0])),
+                        p1 = ex2(fmaf(c[t][n][1], back[n][1], w.off[n][1])),
+                        p2 = ex2(fmaf(c[t][n][2], back[n][0], w.off[n][0])),
+                        p3 = ex2(fmaf(c[t][n][3], back[n][1], w.off[n][1]));
+            w.l[n][0] += p0 + p2;
+            w.l[n][1] += p1 + p3;
+            p[n][0] = movmatrix_trans(pack_f16(p0, p1));
+            p[n][1] = movmatrix_trans(pack_f16(p2, p3));
+          }
+          tile_values<NT>(at + t * kKv4TileBytes, lane, seen[t][0], seen[t][1], p, w.o);
+        }
       }
       __syncwarp();  // every lane has read the slot
       if (issued < count) {
-        issue(issued, slot);
-        if ((++issued & 31) == 0) {
-          ta = na, tb = nb;
-          na = tile_of(issued + 32 + (int)lane, 0);
-          nb = tile_of(issued + 32 + (int)lane, 1);
+        if ((issued & 7) == 0) {
+          tile = ahead;
+          join = joined(tile);
+          ahead = tile_of(kTiles * (issued + 8) + (int)lane);
         }
+        issue(issued, slot);
+        ++issued;
       }
       if (++slot == kRing) slot = 0, parity ^= 1u;
     }
@@ -534,14 +601,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : kCtasPerSm
   }
 }
 
-// One warp per output head: joins the segments of its two columns.
+// One CTA per output head: its warps take the segments of the two columns in
+// turn, four at a time (so that up to 16 segments cost one trip to memory),
+// and the first warp joins what they found.
 constexpr int kCombineWarps = 4;
+constexpr int kAtOnce = 4;
 
 __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const Kv4Args a) {
-  const int lane = (int)(threadIdx.x & 31);
-  const long long id = (long long)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-  if (id >= (long long)a.batch * a.out_heads) return;
-  const int b = (int)(id / a.out_heads), p = (int)(id - (long long)b * a.out_heads);
+  __shared__ float4 sh_o[kCombineWarps][2][32];
+  __shared__ float4 sh_ml[kCombineWarps];
+  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+  const int b = (int)(blockIdx.x / (unsigned)a.out_heads);
+  const int p = (int)blockIdx.x - b * a.out_heads;
   int unit, col;
   if (a.v1) {
     unit = p;
@@ -553,74 +624,101 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
   }
   const int units = a.heads * a.chunks;
   const int n_b = stages_of(a, b);
-  const long long before = stages_before(a, b);
-  const long long run = run_length(a, stages_before(a, a.batch) * units);
+  long long before, total;
+  stage_sums(a, b, before, total);
+  const long long run = run_length(a, total * units);
+  const long long start = before * units + (long long)unit * n_b;
+  const int w0 = (int)divide(start, run);
+  const int n = n_b > 0 ? (int)divide(start + n_b - 1, run) - w0 + 1 : 0;
+  const long long slot0 = (long long)b * units + unit + w0;
+  const float* ml = a.part_ml + (slot0 * a.cols + col) * 2;
+  const float* po = a.part_o + (slot0 * a.cols + col) * kD + 4 * lane;
+  const int64_t ml_step = 2 * a.cols, po_step = (int64_t)a.cols * kD;
+  const float lam = a.lambda[p];
+  float gain[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) gain[i] = a.gain ? a.gain[4 * lane + i] : 1.f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float o[4] = {0.f, 0.f, 0.f, 0.f};
-  if (n_b > 0) {
-    const long long start = before * units + (long long)unit * n_b;
-    const int w0 = (int)(start / run), w1 = (int)((start + n_b - 1) / run);
-    const long long slot0 = (long long)b * units + unit + w0;
-    const int n = w1 - w0 + 1;
-    const float* ml = a.part_ml + (slot0 * a.cols + col) * 2;
-    const float* po = a.part_o + (slot0 * a.cols + col) * kD + 4 * lane;
-    const int64_t ml_step = 2 * a.cols, po_step = (int64_t)a.cols * kD;
-    float m[2] = {kNoMax, kNoMax};
-    for (int s = lane; s < n; s += 32) {
-      const float4 v = *reinterpret_cast<const float4*>(ml + s * ml_step);
-      m[0] = fmaxf(m[0], v.x), m[1] = fmaxf(m[1], v.z);
+  float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, o[2][4] = {};
+  for (int s0 = warp; s0 < n; s0 += kCombineWarps * kAtOnce) {
+    float4 v[kAtOnce], x[kAtOnce], y[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int s = s0 + k * kCombineWarps;
+      v[k] = make_float4(kNoMax, 0.f, kNoMax, 0.f);
+      x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < n) {
+        v[k] = *reinterpret_cast<const float4*>(ml + s * ml_step);
+        x[k] = *reinterpret_cast<const float4*>(po + s * po_step);
+        y[k] = *reinterpret_cast<const float4*>(po + s * po_step + kD);
+      }
     }
+    const float old0 = m[0], old1 = m[1];
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], off));
-      m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], off));
-    }
-    float l[2] = {0.f, 0.f}, acc[2][4] = {};
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float4 v = *reinterpret_cast<const float4*>(ml + s * ml_step);
-      const float f0 = ex2(v.x - m[0]), f1 = ex2(v.z - m[1]);
-      const float4 x = *reinterpret_cast<const float4*>(po + s * po_step);
-      const float4 y = *reinterpret_cast<const float4*>(po + s * po_step + kD);
-      l[0] = fmaf(v.y, f0, l[0]), l[1] = fmaf(v.w, f1, l[1]);
-      acc[0][0] = fmaf(x.x, f0, acc[0][0]), acc[0][1] = fmaf(x.y, f0, acc[0][1]);
-      acc[0][2] = fmaf(x.z, f0, acc[0][2]), acc[0][3] = fmaf(x.w, f0, acc[0][3]);
-      acc[1][0] = fmaf(y.x, f1, acc[1][0]), acc[1][1] = fmaf(y.y, f1, acc[1][1]);
-      acc[1][2] = fmaf(y.z, f1, acc[1][2]), acc[1][3] = fmaf(y.w, f1, acc[1][3]);
-    }
-    const float lam = a.lambda[p];
-    // No token left by the mask: 0.
-    const float r0 = l[0] == 0.f ? 0.f : 1.f / l[0], r1 = l[1] == 0.f ? 0.f : lam / l[1];
+    for (int k = 0; k < kAtOnce; ++k) m[0] = fmaxf(m[0], v[k].x), m[1] = fmaxf(m[1], v[k].z);
+    const float g0 = ex2(old0 - m[0]), g1 = ex2(old1 - m[1]);
+    l[0] *= g0, l[1] *= g1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = acc[0][i] * r0 - acc[1][i] * r1;
-    if (a.apply_norm) {
-      float ss = o[0] * o[0] + o[1] * o[1] + o[2] * o[2] + o[3] * o[3];
+    for (int i = 0; i < 4; ++i) o[0][i] *= g0, o[1][i] *= g1;
 #pragma unroll
-      for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      const float f = a.post_scale * rsqrtf(ss * (1.f / kD) + a.eps);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] *= f * (a.gain ? a.gain[4 * lane + i] : 1.f);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float f0 = ex2(v[k].x - m[0]), f1 = ex2(v[k].z - m[1]);
+      l[0] = fmaf(v[k].y, f0, l[0]), l[1] = fmaf(v[k].w, f1, l[1]);
+      o[0][0] = fmaf(x[k].x, f0, o[0][0]), o[0][1] = fmaf(x[k].y, f0, o[0][1]);
+      o[0][2] = fmaf(x[k].z, f0, o[0][2]), o[0][3] = fmaf(x[k].w, f0, o[0][3]);
+      o[1][0] = fmaf(y[k].x, f1, o[1][0]), o[1][1] = fmaf(y[k].y, f1, o[1][1]);
+      o[1][2] = fmaf(y[k].z, f1, o[1][2]), o[1][3] = fmaf(y[k].w, f1, o[1][3]);
     }
   }
-  *reinterpret_cast<uint2*>(a.out + id * kD + 4 * lane) =
-      make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+  const int warps = n < kCombineWarps ? n : kCombineWarps;  // that had a segment
+  if (warp > 0 && warp < warps) {
+    sh_o[warp][0][lane] = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+    sh_o[warp][1][lane] = make_float4(o[1][0], o[1][1], o[1][2], o[1][3]);
+    if (lane == 0) sh_ml[warp] = make_float4(m[0], l[0], m[1], l[1]);
+  }
+  if (n > 1) __syncthreads();
+  if (warp > 0) return;
+  for (int w = 1; w < warps; ++w) {
+    const float4 v = sh_ml[w], x = sh_o[w][0][lane], y = sh_o[w][1][lane];
+    const float t0 = fmaxf(m[0], v.x), t1 = fmaxf(m[1], v.z);
+    const float g0 = ex2(m[0] - t0), g1 = ex2(m[1] - t1), f0 = ex2(v.x - t0), f1 = ex2(v.z - t1);
+    m[0] = t0, m[1] = t1;
+    l[0] = l[0] * g0 + v.y * f0, l[1] = l[1] * g1 + v.w * f1;
+    o[0][0] = o[0][0] * g0 + x.x * f0, o[0][1] = o[0][1] * g0 + x.y * f0;
+    o[0][2] = o[0][2] * g0 + x.z * f0, o[0][3] = o[0][3] * g0 + x.w * f0;
+    o[1][0] = o[1][0] * g1 + y.x * f1, o[1][1] = o[1][1] * g1 + y.y * f1;
+    o[1][2] = o[1][2] * g1 + y.z * f1, o[1][3] = o[1][3] * g1 + y.w * f1;
+  }
+  // No token left by the mask: 0.
+  const float r0 = l[0] == 0.f ? 0.f : 1.f / l[0], r1 = l[1] == 0.f ? 0.f : lam / l[1];
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = o[0][i] * r0 - o[1][i] * r1;
+  if (a.apply_norm && n > 0) {
+    float ss = y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float f = a.post_scale * rsqrtf(ss * (1.f / kD) + a.eps);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] *= f * gain[i];
+  }
+  *reinterpret_cast<uint2*>(a.out + (size_t)blockIdx.x * kD + 4 * lane) =
+      make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int runs_of(int cols) {
-  return kPlanSms * (cols > 8 ? kCtasPerSmWide : kCtasPerSm) * kWarps;
-}
+constexpr int kRuns = kPlanSms * kCtasPerSm * kWarps;
 
 size_t workspace_bytes_of(int batch, int units, int cols) {
-  const size_t slots = (size_t)batch * units + runs_of(cols);
+  const size_t slots = (size_t)batch * units + kRuns;
   return slots * cols * (kD + 2) * sizeof(float);
 }
 
 int chunks_of(int group) { return (group + kChunkHeads - 1) / kChunkHeads; }
 
 cudaError_t launch(Kv4Args& a, void* workspace, cudaStream_t stream) {
-  a.runs = runs_of(a.cols);
+  a.runs = kRuns;
   const size_t slots = (size_t)a.batch * a.heads * a.chunks + a.runs;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + slots * a.cols * kD;
@@ -637,9 +735,8 @@ cudaError_t launch(Kv4Args& a, void* workspace, cudaStream_t stream) {
   else if (a.cols <= 8) e = run(kv4_decode_kernel<1, false>);
   else e = run(kv4_decode_kernel<2, false>);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)a.batch * a.out_heads;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps));
+  cfg.gridDim = dim3((unsigned)a.batch * (unsigned)a.out_heads);
   cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

@@ -1,5 +1,6 @@
 // kv4_cache.cu — writing rows into the 4-bit paged KV cache and reading them
-// back (formats and layout: kv4.cuh).
+// back (formats and layout: kv4.cuh).  Both are bound by memory: the rows
+// (256 bytes of bf16 a token and head, K and V each) once, 72 bytes held once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,41 +29,50 @@ struct CacheArgs {
   int* dev_status;
 };
 
-// Sixteen consecutive channels as fp32.
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+// Sixteen consecutive channels as they are held, and as fp32 pairs.
+template <typename T>
+struct Block {
+  uint4 v[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Block<T> load_block(const T* p) {
+  Block<T> b;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i) b.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return b;
+}
+__device__ __forceinline__ void unpack(const Block<float>& b, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 f = reinterpret_cast<const float4*>(p)[i];
-    x[4 * i] = f.x;
-    x[4 * i + 1] = f.y;
-    x[4 * i + 2] = f.z;
-    x[4 * i + 3] = f.w;
+    x[4 * i] = __uint_as_float(b.v[i].x), x[4 * i + 1] = __uint_as_float(b.v[i].y);
+    x[4 * i + 2] = __uint_as_float(b.v[i].z), x[4 * i + 3] = __uint_as_float(b.v[i].w);
   }
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+__device__ __forceinline__ void unpack(const Block<__nv_bfloat16>& b, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 w = reinterpret_cast<const uint4*>(p)[i];
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t u[4] = {b.v[i].x, b.v[i].y, b.v[i].z, b.v[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = bf16lo(u[j]);
-      x[8 * i + 2 * j + 1] = bf16hi(u[j]);
-    }
+    for (int j = 0; j < 4; ++j) x[8 * i + 2 * j] = bf16lo(u[j]), x[8 * i + 2 * j + 1] = bf16hi(u[j]);
   }
 }
-__device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
+// Bits of the largest magnitude: infinities and NaN order above every number.
+__device__ __forceinline__ uint32_t amax_bits(const Block<float>& b) {
+  uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(p)[i] =
-        make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    m = max(max(m, max(b.v[i].x & 0x7FFFFFFFu, b.v[i].y & 0x7FFFFFFFu)),
+            max(b.v[i].z & 0x7FFFFFFFu, b.v[i].w & 0x7FFFFFFFu));
+  return m;
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) {
+__device__ __forceinline__ uint32_t amax_bits(const Block<__nv_bfloat16>& b) {
+  uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    reinterpret_cast<uint4*>(p)[i] =
-        make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                   pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+  for (int i = 0; i < 2; ++i) {
+    m = __vmaxu2(m, __vmaxu2(b.v[i].x & 0x7FFF7FFFu, b.v[i].y & 0x7FFF7FFFu));
+    m = __vmaxu2(m, __vmaxu2(b.v[i].z & 0x7FFF7FFFu, b.v[i].w & 0x7FFF7FFFu));
+  }
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
 // Block scale: amax / 6 rounded to the nearest scale (ties to even).  The
@@ -83,98 +93,138 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   return b > (uint32_t)kKv4MaxScale ? (uint32_t)kKv4MaxScale : b;
 }
 
-__device__ __forceinline__ uint8_t* tile_of(const CacheArgs& a, int slot, int head) {
-  const int ps = 1 << a.page_shift;
-  const int64_t page = slot >> a.page_shift;
-  const int tile = (slot & (ps - 1)) >> 4;
-  return a.cache + ((page * a.heads + head) * (ps >> 4) + tile) * kKv4TileBytes;
-}
+// x / s for the codes, near enough that rounding to a level gives what the
+// exact quotient gives.  Borders between levels have 3 significant bits and
+// scales 4, so border * s has 7.
+//  bf16 rows (8 bits): an x that is not on a border is off it by 2^-9 of it or
+//  more, so the product with 1 / s (off by 2^-23 of itself) is rounded to
+//  multiples of 2^-12, which puts ties back on the border and moves nothing
+//  across one.
+//  fp32 rows: an x may be one step off a border.  Only the correctly rounded
+//  quotient falls on the right side then.
+struct Quotient {
+  float s, inv;
+  __device__ __forceinline__ float of(float x, const __nv_bfloat16*) const {
+    return __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 3072.f), -3072.f);
+  }
+  __device__ __forceinline__ float of(float x, const float*) const { return __fdiv_rn(x, s); }
+};
 
-// One thread per block of 16 channels of a (token, head)'s K and V row.
-// A code is x / scale rounded to the nearest level (ties to the even code).
-// As above, the correctly rounded quotient falls on the same side of a border
-// as the exact one: border * scale has 7 significant bits.
+// Work of both kernels: a CTA takes 16 tokens and walks over the KV heads.
+// A warp has 8 tokens and 4 of the 8 blocks of a row of K or of V, so that 4
+// lanes read 128 bytes in a row and, where the 8 tokens lie in a row of slots,
+// the codes of V are written 64 bytes in a row.
+constexpr int kTokens = 16;
+
+struct Lane {
+  int tok, blk, t;   // token, block, place in the tile
+  bool is_v;
+  uint32_t codes, scale;  // bytes of the tile
+  uint8_t* tile;     // of KV head 0
+  int64_t head_bytes;
+  // False if there is nothing to do for this lane's token.
+  __device__ __forceinline__ bool init(const CacheArgs& a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    is_v = warp & 1;
+    blk = 4 * ((warp >> 1) & 1) + (lane & 3);
+    tok = (int)blockIdx.x * kTokens + 8 * (warp >> 2) + (lane >> 2);
+    if (tok >= a.tokens) return false;
+    const int slot = a.slots[tok];
+    if (slot < 0) return false;
+    if (slot >= a.n_slots) {
+      report(a.dev_status, DA_ERR_PAGE);
+      return false;
+    }
+    const int sh = a.page_shift - 4;
+    const int64_t page = slot >> a.page_shift;
+    const int in_page = (slot >> 4) & ((1 << sh) - 1);
+    head_bytes = (int64_t)kKv4TileBytes << sh;
+    tile = a.cache + page * a.heads * head_bytes + in_page * kKv4TileBytes;
+    t = slot & 15;
+    codes = is_v ? kKv4VCodes + 512 * (t >> 3) + 64 * blk + 16 * ((t & 7) >> 1) + 8 * (t & 1)
+                 : t * 64 + blk * 8;
+    scale = is_v ? kKv4VScales + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)
+                 : kKv4KScales + 16 * (t & 7) + 4 * (blk >> 1) + 2 * (t >> 3) + (blk & 1);
+    return true;
+  }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a) {
-  const int blk = threadIdx.x & 7;
-  const int kv = (threadIdx.x >> 3) & 1;
-  const unsigned th = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-  const int tok = (int)(th / (unsigned)a.heads);
-  if (tok >= a.tokens) return;
-  const int head = (int)(th - (unsigned)tok * (unsigned)a.heads);
-  const int slot = a.slots[tok];
-  if (slot < 0) return;
-  if (slot >= a.n_slots) {
-    report(a.dev_status, DA_ERR_PAGE);
-    return;
-  }
-  float x[16];
-  const T* src = kv ? static_cast<const T*>(a.v) + tok * a.v_tok
-                    : static_cast<const T*>(a.k) + tok * a.k_tok;
-  load16(src + head * kKv4Row + blk * 16, x);
-  uint32_t amax = 0u;  // as bits: infinities and NaN order above every finite magnitude
+  Lane w;
+  if (!w.init(a)) return;
+  const T* src = (w.is_v ? static_cast<const T*>(a.v) + w.tok * a.v_tok
+                         : static_cast<const T*>(a.k) + w.tok * a.k_tok) + w.blk * 16;
+  int h = blockIdx.y;
+  Block<T> next = load_block(src + (int64_t)h * kKv4Row);
+  for (; h < a.heads; h += gridDim.y) {
+    const Block<T> b = next;
+    if (h + (int)gridDim.y < a.heads)
+      next = load_block(src + (int64_t)(h + gridDim.y) * kKv4Row);
+    const uint32_t sb = scale_byte(amax_bits(b));
+    uint32_t c[2] = {0u, 0u};
+    if (sb != 0u && sb != (uint32_t)kKv4BadScale) {
+      float x[16];
+      unpack(b, x);
+      const float s = kv4_scale_value(sb);
+      const Quotient q{s, __frcp_rn(s)};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  const uint32_t sb = scale_byte(amax);
-  const float s = kv4_scale_value(sb);
-  uint32_t w[2] = {0u, 0u};
-  if (sb != 0u && sb != (uint32_t)kKv4BadScale) {
+      for (int i = 0; i < 8; ++i)
+        c[i >> 2] |= f32x2_to_e2m1(q.of(x[2 * i], (const T*)nullptr),
+                                   q.of(x[2 * i + 1], (const T*)nullptr)) << (8 * (i & 3));
+    }
+    uint8_t* tile = w.tile + h * w.head_bytes;
+    *reinterpret_cast<uint2*>(tile + w.codes) = make_uint2(c[0], c[1]);
+    tile[w.scale] = (uint8_t)sb;
+  }
+}
+
+__device__ __forceinline__ void store_block(float* p, const uint32_t (&h)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= f32x2_to_e2m1(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s))
-                   << (8 * (i & 3));
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
+    reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
   }
-  uint8_t* tile = tile_of(a, slot, head);
-  const int t = slot & 15;
-  if (kv == 0) {
-    *reinterpret_cast<uint2*>(tile + t * 64 + blk * 8) = make_uint2(w[0], w[1]);
-    tile[kKv4KScales + 16 * (t & 7) + 4 * (blk >> 1) + 2 * (t >> 3) + (blk & 1)] = (uint8_t)sb;
-  } else {
-    *reinterpret_cast<uint2*>(tile + kKv4VCodes + 512 * (t >> 3) + 64 * blk +
-                              16 * ((t & 7) >> 1) + 8 * (t & 1)) = make_uint2(w[0], w[1]);
-    tile[kKv4VScales + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)] = (uint8_t)sb;
+}
+__device__ __forceinline__ void store_block(__nv_bfloat16* p, const uint32_t (&h)[8]) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    u[i] = pack_bf16(a.x, a.y);
   }
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
-  const int blk = threadIdx.x & 7;
-  const int kv = (threadIdx.x >> 3) & 1;
-  const unsigned th = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-  const int tok = (int)(th / (unsigned)a.heads);
-  if (tok >= a.tokens) return;
-  const int head = (int)(th - (unsigned)tok * (unsigned)a.heads);
-  const int slot = a.slots[tok];
-  if (slot < 0) return;
-  if (slot >= a.n_slots) {
-    report(a.dev_status, DA_ERR_PAGE);
-    return;
-  }
-  const uint8_t* tile = tile_of(a, slot, head);
-  const int t = slot & 15;
-  uint2 w;
-  uint32_t sb;
-  if (kv == 0) {
-    w = *reinterpret_cast<const uint2*>(tile + t * 64 + blk * 8);
-    sb = tile[kKv4KScales + 16 * (t & 7) + 4 * (blk >> 1) + 2 * (t >> 3) + (blk & 1)];
-  } else {
-    w = *reinterpret_cast<const uint2*>(tile + kKv4VCodes + 512 * (t >> 3) + 64 * blk +
-                                        16 * ((t & 7) >> 1) + 8 * (t & 1));
-    sb = tile[kKv4VScales + 16 * blk + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1)];
-  }
-  const float s = kv4_scale_value(sb);
-  uint32_t h[8];
-  e2m1x8_to_f16x2(w.x, h[0], h[1], h[2], h[3]);
-  e2m1x8_to_f16x2(w.y, h[4], h[5], h[6], h[7]);
-  float x[16];
+  Lane w;
+  if (!w.init(a)) return;
+  T* dst = static_cast<T*>(w.is_v ? a.v_out : a.k_out) + (int64_t)w.tok * a.heads * kKv4Row +
+           w.blk * 16;
+  int h = blockIdx.y;
+  auto fetch = [&](int head, uint2& c, uint32_t& sb) {
+    const uint8_t* tile = w.tile + head * w.head_bytes;
+    c = *reinterpret_cast<const uint2*>(tile + w.codes);
+    sb = tile[w.scale];
+  };
+  uint2 c_next;
+  uint32_t s_next;
+  fetch(h, c_next, s_next);
+  for (; h < a.heads; h += gridDim.y) {
+    const uint2 c = c_next;
+    const uint32_t s = (s_next << 7) * 0x10001u;  // the scale twice, fp16
+    if (h + (int)gridDim.y < a.heads) fetch(h + gridDim.y, c_next, s_next);
+    uint32_t x[8];
+    e2m1x8_to_f16x2(c.x, x[0], x[1], x[2], x[3]);
+    e2m1x8_to_f16x2(c.y, x[4], x[5], x[6], x[7]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    x[2 * i] = f.x * s;
-    x[2 * i + 1] = f.y * s;
+    for (int i = 0; i < 8; ++i)  // exact in fp16
+      asm("mul.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(s));
+    store_block(dst + (int64_t)h * kKv4Row, x);
   }
-  T* dst = static_cast<T*>(kv ? a.v_out : a.k_out);
-  store16(dst + ((int64_t)tok * a.heads + head) * kKv4Row + blk * 16, x);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -192,8 +242,13 @@ int check(const int* slots, int tokens, int heads, int head_dim, const void* cac
   return DA_OK;
 }
 
-unsigned blocks_for(int tokens, int heads) {
-  return (unsigned)(((long long)tokens * heads * 16 + kThreads - 1) / kThreads);
+// Heads are walked by a CTA where there are CTAs enough for the GPU without
+// (a thread's next row is then in flight while it packs this one), and spread
+// over CTAs otherwise.
+dim3 grid_for(int tokens, int heads) {
+  dim3 g((unsigned)((tokens + kTokens - 1) / kTokens), 1, 1);
+  while ((int)g.y < heads && (long long)g.x * g.y < 148 * 6 && g.y < 65535u) ++g.y;
+  return g;
 }
 
 }  // namespace
@@ -234,7 +289,7 @@ extern "C" int diffattn_kv4_append(const void* k, long long k_token_stride, cons
   a.page_shift = da::kv4_shift(page_size);
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const unsigned grid = da::blocks_for(tokens, n_kv_heads);
+  const dim3 grid = da::grid_for(tokens, n_kv_heads);
   if (dtype == DA_BF16)
     da::kv4_append_kernel<__nv_bfloat16><<<grid, da::kThreads, 0, cs>>>(a);
   else
@@ -261,7 +316,7 @@ extern "C" int diffattn_kv4_read(const void* cache, int n_pages, int page_size, 
   a.page_shift = da::kv4_shift(page_size);
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const unsigned grid = da::blocks_for(tokens, n_kv_heads);
+  const dim3 grid = da::grid_for(tokens, n_kv_heads);
   if (dtype == DA_BF16)
     da::kv4_read_kernel<__nv_bfloat16><<<grid, da::kThreads, 0, cs>>>(a);
   else

@@ -130,8 +130,38 @@ __device__ __forceinline__ void load_angles(const float* cs, const float* sn, fl
   load8(sn, s);
 }
 
+// The weights and the token's angles as coefficients of a thread's 8 pairs:
+// a' = r (a ac - b bs), b' = r (b bc + a as).
+struct Coefs {
+  float ac[8], bs[8], bc[8], as[8];
+};
+
+template <bool kInterleaved>
+__device__ __forceinline__ void fold(const float* w, int o0, int o1, const float (&c)[8],
+                                     const float (&s)[8], Coefs& f) {
+  float g[16];
+  if (w) {
+    load8(w + o0, g);
+    load8(w + o1, g + 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float wa = g[kInterleaved ? 2 * i : i], wb = g[kInterleaved ? 2 * i + 1 : 8 + i];
+    f.ac[i] = wa * c[i], f.bs[i] = wb * s[i], f.bc[i] = wb * c[i], f.as[i] = wa * s[i];
+  }
+}
+
+template <typename T>
+struct Row {
+  uint4 v[sizeof(T)];  // 16 features: two pieces of 8
+};
+
 template <typename T, int G, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    qk_norm_rope_kernel(const NormArgs a) {
   __shared__ __align__(16) float cs[kAngles];
   __shared__ __align__(16) float sn[kAngles];
   const int j = threadIdx.x % G, g = threadIdx.x / G;
@@ -145,20 +175,22 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormArgs a
   int o0, o1;
   bool turned;
   pieces<kInterleaved>(j, a.rot, o0, o1, turned);
-  float x[16];
+  constexpr int kHalf = sizeof(T) / 2;  // 16-byte words of a piece
   auto fetch = [&](int head) {
+    Row<T> r{};
     if (mine && head < heads) {
       const int kind = head >= a.heads[0];
       const T* p = static_cast<const T*>(a.x[kind]) + tok * a.x_tok[kind] +
                    (int64_t)(head - (kind ? a.heads[0] : 0)) * a.d;
-      load8(p + o0, x);
-      load8(p + o1, x + 8);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.f;
+      for (int i = 0; i < kHalf; ++i) {
+        r.v[i] = reinterpret_cast<const uint4*>(p + o0)[i];
+        r.v[kHalf + i] = reinterpret_cast<const uint4*>(p + o1)[i];
+      }
     }
+    return r;
   };
-  fetch(h);  // in flight while the angles are computed
+  Row<T> next = fetch(h);  // in flight while the angles are computed
   angles(a, (int)blockIdx.x << a.tok_log2, cs, sn);
   __syncthreads();
   float c[8], s[8];
@@ -168,35 +200,39 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
   }
+  Coefs f;
+  int kind = -1;
+  const float inv_d = 1.0f / (float)a.d;
   // Every group of the CTA takes the same number of turns: the shuffles of a
   // warp need all its lanes.
   const int first = per_tok * (int)blockIdx.y;
   for (int base = first; base < heads; base += step, h += step) {
+    float x[16];
+    load8(reinterpret_cast<const T*>(&next.v[0]), x);
+    load8(reinterpret_cast<const T*>(&next.v[kHalf]), x + 8);
+    if (base + step < heads) next = fetch(h + step);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    const float r = rsqrtf(group_sum<G>(ss) / (float)a.d + a.eps);
+    const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
     if (mine && h < heads) {
-      const int kind = h >= a.heads[0];
-      const float* w = a.w[kind];
-      float y[16];
-      if (w) {
-        float g0[16];
-        load8(w + o0, g0);
-        load8(w + o1, g0 + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = x[i] * r * g0[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = x[i] * r;
+      const int k = h >= a.heads[0];
+      if (k != kind) {  // once for the queries, once for the keys
+        kind = k;
+        fold<kInterleaved>(a.w[k], o0, o1, c, s, f);
       }
-      if (turned) rotate<kInterleaved>(y, c, s, 1.f);
-      T* p = static_cast<T*>(a.y[kind]) + tok * a.y_tok[kind] +
-             (int64_t)(h - (kind ? a.heads[0] : 0)) * a.d;
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = x[kInterleaved ? 2 * i : i], v = x[kInterleaved ? 2 * i + 1 : 8 + i];
+        y[kInterleaved ? 2 * i : i] = r * (u * f.ac[i] - v * f.bs[i]);
+        y[kInterleaved ? 2 * i + 1 : 8 + i] = r * (v * f.bc[i] + u * f.as[i]);
+      }
+      T* p = static_cast<T*>(a.y[k]) + tok * a.y_tok[k] +
+             (int64_t)(h - (k ? a.heads[0] : 0)) * a.d;
       store8(p + o0, y);
       store8(p + o1, y + 8);
     }
-    if (base + step < heads) fetch(h + step);
   }
 }
 
@@ -206,8 +242,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormArgs a
 // bits.  The order depends on the sizes alone.
 template <typename T, int G, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const NormArgs a) {
-  __shared__ __align__(16) float cs[kAngles];
-  __shared__ __align__(16) float sn[kAngles];
+  __shared__ __align__(16) float cs[2][kAngles];
+  __shared__ __align__(16) float sn[2][kAngles];
   __shared__ float sums[kThreads / 32][2 * 256];
   const int j = threadIdx.x % G, g = threadIdx.x / G;
   const int per_tok = (kThreads / G) >> a.tok_log2;
@@ -221,15 +257,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const Nor
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
   const int batches = (a.tokens + (1 << a.tok_log2) - 1) >> a.tok_log2;
-  for (int batch = blockIdx.x; batch < batches; batch += gridDim.x) {
-    const int tok0 = batch << a.tok_log2;
-    const int tok = tok0 + t;
-    __syncthreads();
-    angles(a, tok0, cs, sn);
-    __syncthreads();
+  angles(a, (int)blockIdx.x << a.tok_log2, cs[0], sn[0]);
+  for (int batch = blockIdx.x, turn = 0; batch < batches; batch += gridDim.x, ++turn) {
+    const int tok = (batch << a.tok_log2) + t;
+    const int buf = turn & 1;
+    __syncthreads();  // this batch's angles are there, the other buffer is free
+    if (batch + (int)gridDim.x < batches)
+      angles(a, (batch + (int)gridDim.x) << a.tok_log2, cs[buf ^ 1], sn[buf ^ 1]);
     float c[8], s[8];
     if (turned) {
-      load_angles(cs + t * (a.rot >> 1) + 8 * j, sn + t * (a.rot >> 1) + 8 * j, c, s);
+      load_angles(cs[buf] + t * (a.rot >> 1) + 8 * j, sn[buf] + t * (a.rot >> 1) + 8 * j, c, s);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
@@ -386,7 +423,7 @@ int batch_log2(int tokens, int heads, int lanes, int rot, int enough) {
   auto room = [&](int ctas) {
     return (rot << lg) <= kAngles && (tokens >> (lg + 1)) >= ctas && (groups >> (lg + 1)) >= 1;
   };
-  while (room(148) && (groups >> lg) > heads) ++lg;
+  while (room(148) && (groups >> (lg + 1)) >= heads) ++lg;
   while (lg < 2 && room(enough)) ++lg;
   return lg;
 }

@@ -60,6 +60,7 @@ EXPORTS = (
     "diffattn_v2_bwd_saved",
     "diffattn_v2_prefill_oproj_workspace_size",
     "diffattn_v2_prefill_oproj",
+    "diffattn_page_plan_workspace_size",
     "diffattn_page_plan",
     "diffattn_page_release",
     "diffattn_kv4_page_bytes",
@@ -178,7 +179,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.diffattn_v2_prefill_oproj.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                                               _i, _i, _i, _i, _vp, _sz, _vp, _vp]
     lib.diffattn_page_plan.restype = _i
-    lib.diffattn_page_plan.argtypes = [_vp] * 5 + [_i] * 5 + [_vp] * 8
+    lib.diffattn_page_plan.argtypes = [_vp] * 5 + [_i] * 5 + [_vp] * 7 + [_sz, _vp, _vp]
+    lib.diffattn_page_plan_workspace_size.restype = _sz
+    lib.diffattn_page_plan_workspace_size.argtypes = [_i, _i]
     lib.diffattn_page_release.restype = _i
     lib.diffattn_page_release.argtypes = [_vp] * 5 + [_i] * 4 + [_vp] * 2
     lib.diffattn_kv4_page_bytes.restype = _sz
@@ -746,8 +749,12 @@ def _page_lists(first, cache_lens, block_table, free_pages, free_count):
     return R, block_table.shape[1], free_pages.shape[0]
 
 
+def diffattn_page_plan_workspace_size(requests, n_slots) -> int:
+    return int(load().diffattn_page_plan_workspace_size(requests, n_slots))
+
+
 def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count, page_size,
-                       n_slots, *, out=None, dev_status=None, stream=None):
+                       n_slots, *, out=None, workspace=None, dev_status=None, stream=None):
     """Pages, slots and positions of a step's new tokens.  new_lens,
     cache_lens int32 [R]; block_table int32 [R, max_pages] (new pages written
     in place); free_pages int32 [n_pages], a stack of which free_count int32
@@ -759,11 +766,14 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
     _need("new_lens", new_lens, _I32, (R,))
     if n_slots < 0:
         raise ValueError("n_slots is negative")
+    need = 0
+    if workspace is None and n_slots > 1024:   # none below
+        need = diffattn_page_plan_workspace_size(R, n_slots)
     if out is None:
-        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, dev_status)
-        slots, positions, offsets, served, lens, count = torch.empty(
-            2 * n_slots + 3 * R + 2, dtype=_I32, device=new_lens.device).split_with_sizes(
-                (n_slots, n_slots, R + 1, R, R, 1))
+        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, workspace,
+                         dev_status)
+        slots, positions, offsets, served, lens, count = new_lens.new_empty(
+            2 * n_slots + 3 * R + 2).split_with_sizes((n_slots, n_slots, R + 1, R, R, 1))
         out = {"slots": slots, "positions": positions, "offsets": offsets, "served": served,
                "cache_lens": lens, "free_count": count}
     else:
@@ -772,12 +782,15 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
             _need(name, out[name], _I32, (n,))
         slots, positions, offsets, served, lens, count = (out[name] for name in (
             "slots", "positions", "offsets", "served", "cache_lens", "free_count"))
-        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, dev_status,
-                         slots, positions, offsets, served, lens, count)
+        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, workspace,
+                         dev_status, slots, positions, offsets, served, lens, count)
+    if need:
+        workspace = _workspace(None, need, at, stream)
     _run("diffattn_page_plan", at, stream, new_lens.data_ptr(), cache_lens.data_ptr(),
          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
          n_pages, page_size, n_slots, slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
-         served.data_ptr(), lens.data_ptr(), count.data_ptr(), _ptr(dev_status))
+         served.data_ptr(), lens.data_ptr(), count.data_ptr(), _ptr(workspace),
+         0 if workspace is None else workspace.nbytes, _ptr(dev_status))
     return out
 
 
@@ -853,7 +866,7 @@ def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
     max_pages = _decode_lists(B, block_table, cache_lens, lam, Hq // 2)
     at = _one_device(q, cache, block_table, cache_lens, lam, workspace, out, dev_status)
     if out is None:
-        out = torch.empty((B, Hq // 2, d), dtype=q.dtype, device=q.device)
+        out = q.new_empty((B, Hq // 2, d))
     else:
         _need("out", out, q.dtype, (B, Hq // 2, d))
     ws = _workspace(workspace, 0 if workspace is not None else
@@ -896,7 +909,7 @@ def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
     at = _one_device(q, cache, block_table, cache_lens, lam, norm_weight, workspace, out,
                      dev_status)
     if out is None:
-        out = torch.empty((B, H, 128), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     else:
         _need("out", out, q.dtype, (B, H, 128))
     ws = _workspace(workspace, 0 if workspace is not None else
@@ -942,9 +955,10 @@ def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=
                                                       k_weight)
     ko, kos = None, 0
     if out is None:
-        qo, qos = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device), Hq * d
+        # dense, since a token's heads lie in a row and tokens do not overlap
+        qo, qos = torch.empty_like(q), Hq * d
         if k is not None:
-            ko, kos = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device), Hk * d
+            ko, kos = torch.empty_like(k), Hk * d
         at = _one_device(q, k, positions, inv_freq, q_weight, k_weight)
     else:
         qo, ko = out
@@ -978,12 +992,9 @@ def diffattn_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, *, q_we
     gqs = _token_stride("dq_out", dq_out, T, _F32)
     gks = 0 if k is None else _token_stride("dk_out", dk_out, T, _F32)
     at = _one_device(q, k, dq_out, dk_out, positions, inv_freq, q_weight, k_weight, workspace)
-    dev = q.device
-    r = {"dq": torch.empty((T, Hq, d), dtype=_F32, device=dev),
-         "dk": None if k is None else torch.empty((T, Hk, d), dtype=_F32, device=dev),
-         "dq_weight": None if q_weight is None else torch.empty(d, dtype=_F32, device=dev),
-         "dk_weight": None if k is None or k_weight is None else
-         torch.empty(d, dtype=_F32, device=dev)}
+    r = {"dq": torch.empty_like(dq_out), "dk": None if k is None else torch.empty_like(dk_out),
+         "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+         "dk_weight": None if k is None or k_weight is None else torch.empty_like(k_weight)}
     ws = _workspace(workspace, 0 if workspace is not None else
                     diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), at, stream)
     _run("diffattn_qk_norm_rope_bwd", at, stream, q.data_ptr(), qs, _ptr(k), ks, code,

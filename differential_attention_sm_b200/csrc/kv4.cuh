@@ -63,15 +63,18 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t& a, uint32_
       : "r"(w));
 }
 
-// Two floats to a byte of two codes, `lo` in the low nibble (round to nearest
-// even, saturating at 6).
-__device__ __forceinline__ uint32_t f32x2_to_e2m1(float lo, float hi) {
+// Eight floats to a word of codes, the first in the low four bits (round to
+// nearest even, saturating at 6).
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float* x) {
   uint32_t r;
-  asm("{\n\t.reg .b8 x;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\t"
-      "mov.b32 %0, {x, 0, 0, 0};\n\t}"
+  asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x3, %8, %7;\n\t"
+      "mov.b32 %0, {x0, x1, x2, x3};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 

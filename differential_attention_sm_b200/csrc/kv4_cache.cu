@@ -75,13 +75,9 @@ __device__ __forceinline__ uint32_t amax_bits(const Block<__nv_bfloat16>& b) {
   return max(m << 16, m & 0xFFFF0000u);
 }
 
-// Block scale: amax / 6 rounded to the nearest scale (ties to even).  The
-// correctly rounded quotient decides as the exact one would: amax and 6 *
-// (midpoint of two scales) are fp32 numbers, so unless they are equal they
-// differ by an fp32 step of amax, which is more than the quotient's rounding.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-  if (amax_bits >= 0x7F800000u) return (uint32_t)kKv4BadScale;
-  const float t = __fdiv_rn(__uint_as_float(amax_bits), 6.0f);
+// fp32 (a scale before its rounding, >= 0) to the nearest scale's byte, ties to
+// even.
+__device__ __forceinline__ uint32_t scale_byte(float t) {
   uint32_t b;
   if (t < 6.103515625e-5f) {  // below 2^-14 the scales are multiples of 2^-17
     b = (uint32_t)__float2int_rn(t * 131072.0f);
@@ -90,25 +86,47 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
     u += 0x7FFFFu + ((u >> 20) & 1u);
     b = (u >> 20) - ((127u - 15u) << 3);
   }
-  return b > (uint32_t)kKv4MaxScale ? (uint32_t)kKv4MaxScale : b;
+  return min(b, (uint32_t)kKv4MaxScale);
 }
 
-// x / s for the codes, near enough that rounding to a level gives what the
-// exact quotient gives.  Borders between levels have 3 significant bits and
-// scales 4, so border * s has 7.
-//  bf16 rows (8 bits): an x that is not on a border is off it by 2^-9 of it or
-//  more, so the product with 1 / s (off by 2^-23 of itself) is rounded to
-//  multiples of 2^-12, which puts ties back on the border and moves nothing
-//  across one.
-//  fp32 rows: an x may be one step off a border.  Only the correctly rounded
-//  quotient falls on the right side then.
-struct Quotient {
-  float s, inv;
-  __device__ __forceinline__ float of(float x, const __nv_bfloat16*) const {
-    return __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 3072.f), -3072.f);
+// Quotients near enough that rounding them gives what rounding the exact ones
+// gives.  A quotient on a border between two scales or levels belongs to an
+// amax (x) of 7 significant bits: 6 * border has 7, border * scale 3 + 4.
+//  bf16 rows (8 bits): whatever is not on a border is off it by 2^-9 of it or
+//  more, so a product with the reciprocal (off by less than 2^-21 of itself)
+//  is rounded to some 12 bits, which puts ties back on the border and moves
+//  nothing across one.
+//  fp32 rows: a value may be one step off a border.  The correctly rounded
+//  quotient is on the border only if the exact one is, since the step is more
+//  than half a step of the quotient.
+__device__ __forceinline__ float sixth(float amax, const __nv_bfloat16*) {
+  return __uint_as_float((__float_as_uint(amax * (1.0f / 6.0f)) + 0x400u) & 0xFFFFF800u);
+}
+__device__ __forceinline__ float sixth(float amax, const float*) { return __fdiv_rn(amax, 6.0f); }
+
+// Sixteen codes of a block with scale s, 8 bytes.
+__device__ __forceinline__ uint2 codes_of(const Block<__nv_bfloat16>& b, float s) {
+  float x[16];
+  unpack(b, x);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const uint64_t inv2 = f2pack(inv, inv), up = f2pack(3072.f, 3072.f), down = f2pack(-3072.f, -3072.f);
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // to multiples of 2^-12
+    uint64_t v = fma2(f2pack(x[2 * i], x[2 * i + 1]), inv2, f2pack(-0.f, -0.f));
+    v = add2(add2(v, up), down);
+    f2unpack(v, y[2 * i], y[2 * i + 1]);
   }
-  __device__ __forceinline__ float of(float x, const float*) const { return __fdiv_rn(x, s); }
-};
+  return make_uint2(f32x8_to_e2m1(y), f32x8_to_e2m1(y + 8));
+}
+__device__ __forceinline__ uint2 codes_of(const Block<float>& b, float s) {
+  float x[16];
+  unpack(b, x);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], s);
+  return make_uint2(f32x8_to_e2m1(x), f32x8_to_e2m1(x + 8));
+}
 
 // Work of both kernels: a CTA takes 16 tokens and walks over the KV heads.
 // A warp has 8 tokens and 4 of the 8 blocks of a row of K or of V, so that 4
@@ -161,44 +179,56 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a)
     const Block<T> b = next;
     if (h + (int)gridDim.y < a.heads)
       next = load_block(src + (int64_t)(h + gridDim.y) * kKv4Row);
-    const uint32_t sb = scale_byte(amax_bits(b));
-    uint32_t c[2] = {0u, 0u};
-    if (sb != 0u && sb != (uint32_t)kKv4BadScale) {
-      float x[16];
-      unpack(b, x);
-      const float s = kv4_scale_value(sb);
-      const Quotient q{s, __frcp_rn(s)};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        c[i >> 2] |= f32x2_to_e2m1(q.of(x[2 * i], (const T*)nullptr),
-                                   q.of(x[2 * i + 1], (const T*)nullptr)) << (8 * (i & 3));
-    }
+    const uint32_t top = amax_bits(b);
+    const uint32_t sb = top >= 0x7F800000u
+                            ? (uint32_t)kKv4BadScale
+                            : scale_byte(sixth(__uint_as_float(top), (const T*)nullptr));
+    uint2 c = make_uint2(0u, 0u);
+    if (sb != 0u && sb != (uint32_t)kKv4BadScale) c = codes_of(b, kv4_scale_value(sb));
     uint8_t* tile = w.tile + h * w.head_bytes;
-    *reinterpret_cast<uint2*>(tile + w.codes) = make_uint2(c[0], c[1]);
+    *reinterpret_cast<uint2*>(tile + w.codes) = c;
     tile[w.scale] = (uint8_t)sb;
   }
 }
 
-__device__ __forceinline__ void store_block(float* p, const uint32_t (&h)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
-    reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+// 32 bytes in one store (kWide: p is a multiple of 32), or in two: a store of
+// every other 16 bytes leaves half of each sector to the next one.
+template <bool kWide>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8]) {
+  if (kWide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
 }
+template <bool kWide>
+__device__ __forceinline__ void store_block(float* p, const uint32_t (&h)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[4 * i + j]));
+      u[2 * j] = __float_as_uint(f.x), u[2 * j + 1] = __float_as_uint(f.y);
+    }
+    store32<kWide>(p + 8 * i, u);
+  }
+}
+template <bool kWide>
 __device__ __forceinline__ void store_block(__nv_bfloat16* p, const uint32_t (&h)[8]) {
   uint32_t u[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    u[i] = pack_bf16(a.x, a.y);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    u[i] = pack_bf16(f.x, f.y);
   }
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  store32<kWide>(p, u);
 }
 
-template <typename T>
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
   Lane w;
   if (!w.init(a)) return;
@@ -223,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)  // exact in fp16
       asm("mul.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(s));
-    store_block(dst + (int64_t)h * kKv4Row, x);
+    store_block<kWide>(dst + (int64_t)h * kKv4Row, x);
   }
 }
 
@@ -247,7 +277,7 @@ int check(const int* slots, int tokens, int heads, int head_dim, const void* cac
 // over CTAs otherwise.
 dim3 grid_for(int tokens, int heads) {
   dim3 g((unsigned)((tokens + kTokens - 1) / kTokens), 1, 1);
-  while ((int)g.y < heads && (long long)g.x * g.y < 148 * 6 && g.y < 65535u) ++g.y;
+  while ((int)g.y < heads && (long long)g.x * g.y < 148 * 12 && g.y < 65535u) ++g.y;
   return g;
 }
 
@@ -317,9 +347,13 @@ extern "C" int diffattn_kv4_read(const void* cache, int n_pages, int page_size, 
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const dim3 grid = da::grid_for(tokens, n_kv_heads);
-  if (dtype == DA_BF16)
-    da::kv4_read_kernel<__nv_bfloat16><<<grid, da::kThreads, 0, cs>>>(a);
-  else
-    da::kv4_read_kernel<float><<<grid, da::kThreads, 0, cs>>>(a);
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
+  if (dtype == DA_BF16) {
+    if (wide) da::kv4_read_kernel<__nv_bfloat16, true><<<grid, da::kThreads, 0, cs>>>(a);
+    else da::kv4_read_kernel<__nv_bfloat16, false><<<grid, da::kThreads, 0, cs>>>(a);
+  } else {
+    if (wide) da::kv4_read_kernel<float, true><<<grid, da::kThreads, 0, cs>>>(a);
+    else da::kv4_read_kernel<float, false><<<grid, da::kThreads, 0, cs>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }

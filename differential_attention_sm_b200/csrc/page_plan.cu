@@ -10,8 +10,10 @@
 // served takers are a prefix and their stack ranges do not overlap.
 //
 // Bound by latency: a step of 64 requests moves 2 KB.  One CTA does the sums
-// and all state, a row of requests per pass; with few slot rows it also writes
-// them, since every thread holds what its request needs.
+// and all state, a row of requests per pass, and with few slot rows also writes
+// those and the new table entries, since a thread holds what its request
+// needs.  With many (prompts), it leaves each request's depth in the stack in
+// the workspace, and a second kernel writes rows and entries with all SMs.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -40,6 +42,7 @@ struct PlanArgs {
   int* served;
   int* lens_out;
   int* count_out;
+  int* depth;  // [requests], for the second kernel
   int* dev_status;
 };
 
@@ -74,8 +77,9 @@ __device__ __forceinline__ int slot_of(int page, int pos, int shift) {
   return (int)(((unsigned)page << shift) + (unsigned)(pos & ((1 << shift) - 1)));
 }
 
-// `with_slots`: this launch writes the slot rows too.
+// `with_slots`: this launch writes the slot rows and table entries too.
 __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, int with_slots) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ long long sh[33];
   const int tid = threadIdx.x, lane = tid & 31;
   const int ps = 1 << a.page_shift;
@@ -108,13 +112,14 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
       if (r == a.requests - 1) a.offsets[r + 1] = (int)(tok_end < INT_MAX ? tok_end : INT_MAX);
       a.served[r] = ok ? 1 : 0;
       a.lens_out[r] = ok ? (int)after : len;
+      if (!with_slots) a.depth[r] = ok && need ? (int)(free0 - upto + need) : 0;
     }
     // New table entries and slot rows: a thread writes its own request's when
     // they are few, else its whole warp does, one request at a time.
     const int depth = (int)(upto - need);
     const int rows = with_slots && live && tok_at < a.n_slots
                          ? (int)(tok_end < a.n_slots ? n : a.n_slots - tok_at) : 0;
-    const int pages = ok ? need : 0;
+    const int pages = with_slots && ok ? need : 0;
     const bool many = pages > 2 || rows > 2;
     int* row = a.table + (size_t)(live ? r : 0) * a.max_pages;
     if (!many) {
@@ -176,18 +181,30 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
   if (refused) report(a.dev_status, DA_ERR_CACHE_FULL);
 }
 
-// Slot rows of a large step: each thread finds its row's request by bisection
-// over the offsets.  A CTA bisects its first and last row once and then keeps
-// the offsets between them in shared memory when they fit.
+// Slot rows of a large step: a CTA finds the requests of its rows by bisection
+// over the offsets and, if they are few, keeps what it needs of them in shared
+// memory; a thread bisects those for each of its rows.  The row that begins a
+// new page writes its table entry: a new page's first position is a new token's.
 constexpr int kFillThreads = 256;
-constexpr int kFillRows = 2048;
-constexpr int kFillKeep = 1024;
+constexpr int kFillRows = 1024;
+constexpr int kFillKeep = 1536;
 
-__device__ __forceinline__ int upper_request(const int* offsets, int lo, int hi, int i) {
-  // last r in [lo, hi] with offsets[r] <= i
+struct Request {
+  int offset, len, depth;  // the first new page lies below stack[depth]; < 0: not served
+};
+
+__device__ __forceinline__ Request request_of(const PlanArgs& a, int r) {
+  const int n = a.new_lens[r], ok = a.served[r];
+  return {a.offsets[r], (int)((unsigned)a.lens_out[r] - (unsigned)(ok && n > 0 ? n : 0)),
+          ok ? a.depth[r] : -1};
+}
+
+// Last r in [lo, hi] whose offset is at most i.
+template <typename F>
+__device__ __forceinline__ int upper_request(F offset, int lo, int hi, int i) {
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (offsets[mid] <= i) lo = mid;
+    if (offset(mid) <= i) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -195,31 +212,41 @@ __device__ __forceinline__ int upper_request(const int* offsets, int lo, int hi,
 
 __global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs a) {
   __shared__ int ends[2];
-  __shared__ int keep[kFillKeep];
+  __shared__ Request keep[kFillKeep];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int first = blockIdx.x * kFillRows;
   const int last = min(first + kFillRows, a.n_slots) - 1;
+  auto global = [&](int r) { return a.offsets[r]; };
   if (threadIdx.x < 2)
-    ends[threadIdx.x] = upper_request(a.offsets, 0, a.requests - 1, threadIdx.x ? last : first);
+    ends[threadIdx.x] = upper_request(global, 0, a.requests - 1, threadIdx.x ? last : first);
   __syncthreads();
   const int lo = ends[0], hi = ends[1];
   const bool kept = hi - lo < kFillKeep;
   if (kept)
-    for (int r = lo + threadIdx.x; r <= hi; r += kFillThreads) keep[r - lo] = a.offsets[r];
+    for (int r = lo + threadIdx.x; r <= hi; r += kFillThreads) keep[r - lo] = request_of(a, r);
   __syncthreads();
   const int total = a.offsets[a.requests];
+  const int mask = (1 << a.page_shift) - 1;
   for (int i = first + threadIdx.x; i <= last; i += kFillThreads) {
     int slot = -1, pos = 0;
     if (i < total) {
-      const int r = kept ? lo + upper_request(keep, 0, hi - lo, i)
-                         : upper_request(a.offsets, lo, hi, i);
-      const int at = i - a.offsets[r];
-      const int ok = a.served[r];
-      int n = a.new_lens[r];
-      n = n < 0 ? 0 : n;
-      pos = (int)((unsigned)a.lens_out[r] - (unsigned)(ok ? n : 0) + (unsigned)at);
-      if (ok)
-        slot = slot_of(a.table[(size_t)r * a.max_pages + (pos >> a.page_shift)], pos,
-                       a.page_shift);
+      const int r = kept ? lo + upper_request([&](int k) { return keep[k].offset; }, 0, hi - lo, i)
+                         : upper_request(global, lo, hi, i);
+      const Request q = kept ? keep[r - lo] : request_of(a, r);
+      pos = (int)((unsigned)q.len + (unsigned)(i - q.offset));
+      if (q.depth >= 0) {
+        const int blk = pos >> a.page_shift;
+        const int old = (int)(((unsigned)q.len + (unsigned)mask) >> a.page_shift);
+        int* entry = a.table + (size_t)r * a.max_pages + blk;
+        int page;
+        if (blk < old) {
+          page = *entry;
+        } else {
+          page = a.stack[q.depth - 1 - (blk - old)];
+          if ((pos & mask) == 0) *entry = page;
+        }
+        slot = slot_of(page, pos, a.page_shift);
+      }
     }
     a.slots[i] = slot;
     a.positions[i] = pos;
@@ -308,18 +335,28 @@ int check(int requests, int max_pages, int n_pages, int page_size) {
   return DA_OK;
 }
 
-// Slot rows that the one CTA of the plan still writes itself.
-constexpr int kOneCtaRows = 4096;
+// Whether the one CTA of the plan writes the slot rows itself: few rows, or few
+// for each request (a decode step with spare rows).  Measured (one CTA, two
+// kernels): 64 requests and 1024 rows 5.9 and 6.5 us, 2064 rows 9.2 and 6.7,
+// 12864 rows 26 and 7.1; 1500 requests and 6500 rows 7.3 and 9.
+bool one_cta(int requests, int n_slots) {
+  return n_slots <= 16384 && n_slots <= 1024 + 4LL * requests;
+}
 
 }  // namespace
 }  // namespace da
+
+extern "C" size_t diffattn_page_plan_workspace_size(int requests, int n_slots) {
+  if (requests < 1 || da::one_cta(requests, n_slots)) return 0;
+  return (size_t)requests * sizeof(int);
+}
 
 extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, int* block_table,
                                   const int* free_pages, const int* free_count, int requests,
                                   int max_pages, int n_pages, int page_size, int n_slots,
                                   int* slots, int* positions, int* offsets, int* served,
-                                  int* cache_lens_out, int* free_count_out, int* dev_status,
-                                  void* stream) {
+                                  int* cache_lens_out, int* free_count_out, void* workspace,
+                                  size_t workspace_bytes, int* dev_status, void* stream) {
   if (!new_lens || !cache_lens || !block_table || !free_pages || !free_count || !offsets ||
       !served || !cache_lens_out || !free_count_out)
     return DA_ERR_INVALID_ARG;
@@ -327,6 +364,8 @@ extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, in
   const int st = da::check(requests, max_pages, n_pages, page_size);
   if (st != DA_OK) return st;
   if (n_slots > (1 << 30)) return DA_ERR_UNSUPPORTED;
+  const size_t need = diffattn_page_plan_workspace_size(requests, n_slots);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return DA_ERR_WORKSPACE;
   da::PlanArgs a{};
   a.new_lens = new_lens;
   a.lens = cache_lens;
@@ -344,15 +383,23 @@ extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, in
   a.served = served;
   a.lens_out = cache_lens_out;
   a.count_out = free_count_out;
+  a.depth = static_cast<int*>(workspace);
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int one = n_slots <= da::kOneCtaRows;
-  da::page_plan_kernel<<<1, da::threads_for(requests), 0, cs>>>(a, one);
+  da::page_plan_kernel<<<1, da::threads_for(requests), 0, cs>>>(a, need == 0);
   if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
-  if (!one) {
-    const unsigned grid = (unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows);
-    da::page_slots_kernel<<<grid, da::kFillThreads, 0, cs>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
+  if (need > 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows));
+    cfg.blockDim = dim3(da::kFillThreads);
+    cfg.stream = cs;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, da::page_slots_kernel, (const da::PlanArgs)a) != cudaSuccess)
+      return DA_ERR_CUDA;
   }
   return DA_OK;
 }

@@ -468,14 +468,18 @@ DA_API size_t diffattn_kv4_page_bytes(int n_kv_heads, int head_dim, int page_siz
  *                   if not served); may be cache_lens
  *   free_count_out: int32 [1], pages left; may be free_count
  * All device pointers.  slots and positions may be NULL with n_slots = 0.
+ *   workspace     : device scratch of the queried size (0 for up to 1024 slot
+ *                   rows; workspace may be NULL then)
  * Up to 65536 requests and 2^30 slot rows.  DA_ERR_CACHE_FULL goes to dev_status if a request
  * was not served.  The result depends on the arguments' values alone, and a
  * call repeated with the same ones writes the same. */
+DA_API size_t diffattn_page_plan_workspace_size(int requests, int n_slots);
 DA_API int diffattn_page_plan(const int* new_lens, const int* cache_lens, int* block_table,
                               const int* free_pages, const int* free_count, int requests,
                               int max_pages, int n_pages, int page_size, int n_slots, int* slots,
                               int* positions, int* offsets, int* served, int* cache_lens_out,
-                              int* free_count_out, int* dev_status, void* stream);
+                              int* free_count_out, void* workspace, size_t workspace_bytes,
+                              int* dev_status, void* stream);
 
 /* Gives the pages of finished requests back: for each r with release[r] != 0,
  * in order, its ceil(cache_lens[r] / page_size) pages go on the stack, their

@@ -33,6 +33,7 @@ namespace da {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 2;
 constexpr int kAngles = 1024;     // angles of a CTA's batch of tokens
 constexpr int kBwdCtas = 148 * 2; // workspace rows; fixed, so that the size query needs no device
 
@@ -58,18 +59,9 @@ __device__ __forceinline__ void load8(const float* p, float* x) {
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
   x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  x[0] = bf16lo(u.x), x[1] = bf16hi(u.x), x[2] = bf16lo(u.y), x[3] = bf16hi(u.y);
-  x[4] = bf16lo(u.z), x[5] = bf16hi(u.z), x[6] = bf16lo(u.w), x[7] = bf16hi(u.w);
-}
 __device__ __forceinline__ void store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
 // Offsets of a thread's two pieces; `turned` says whether they are rotated.
@@ -131,9 +123,15 @@ __device__ __forceinline__ void load_angles(const float* cs, const float* sn, fl
 }
 
 // The weights and the token's angles as coefficients of a thread's 8 pairs:
-// a' = r (a ac - b bs), b' = r (b bc + a as).
+// a' = r (a wa cos - b wb sin), b' = r (b wb cos + a wa sin).  Held two by two
+// for the packed fp32 instructions, which halve the arithmetic: at one
+// instruction a feature it took as long as the memory (71 us for 16384 tokens
+// of 40 heads where the bytes take 51).
+//  halves:      words 0 .. 3 make a' of two pairs each, words 4 .. 7 b'
+//  interleaved: word i makes (a', b') of pair i
+// out[i] = r (own[i] c[i] + other[i] s[i])
 struct Coefs {
-  float ac[8], bs[8], bc[8], as[8];
+  uint64_t c[8], s[8];
 };
 
 template <bool kInterleaved>
@@ -147,123 +145,144 @@ __device__ __forceinline__ void fold(const float* w, int o0, int o1, const float
 #pragma unroll
     for (int i = 0; i < 16; ++i) g[i] = 1.f;
   }
+  if (kInterleaved) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float wa = g[kInterleaved ? 2 * i : i], wb = g[kInterleaved ? 2 * i + 1 : 8 + i];
-    f.ac[i] = wa * c[i], f.bs[i] = wb * s[i], f.bc[i] = wb * c[i], f.as[i] = wa * s[i];
+    for (int i = 0; i < 8; ++i) {
+      f.c[i] = f2pack(g[2 * i] * c[i], g[2 * i + 1] * c[i]);
+      f.s[i] = f2pack(-g[2 * i + 1] * s[i], g[2 * i] * s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int i = 2 * m, k = i + 1;
+      f.c[m] = f2pack(g[i] * c[i], g[k] * c[k]);
+      f.s[m] = f2pack(-g[8 + i] * s[i], -g[8 + k] * s[k]);
+      f.c[4 + m] = f2pack(g[8 + i] * c[i], g[8 + k] * c[k]);
+      f.s[4 + m] = f2pack(g[i] * s[i], g[k] * s[k]);
+    }
   }
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t x) { return (x << 32) | (x >> 32); }
+
+// Sixteen features as held, and as fp32 pairs.
 template <typename T>
 struct Row {
-  uint4 v[sizeof(T)];  // 16 features: two pieces of 8
+  uint4 v[sizeof(T)];
 };
+__device__ __forceinline__ void unpack(const Row<__nv_bfloat16>& r, uint64_t (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[4 * i + j] = f2pack(bf16lo(u[j]), bf16hi(u[j]));
+  }
+}
+__device__ __forceinline__ void unpack(const Row<float>& r, uint64_t (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = f2pack(__uint_as_float(r.v[i].x), __uint_as_float(r.v[i].y));
+    x[2 * i + 1] = f2pack(__uint_as_float(r.v[i].z), __uint_as_float(r.v[i].w));
+  }
+}
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, const uint64_t* y) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2unpack(y[i], lo, hi);
+    u[i] = pack_bf16(lo, hi);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store_pairs(float* p, const uint64_t* y) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float4 f;
+    f2unpack(y[2 * i], f.x, f.y);
+    f2unpack(y[2 * i + 1], f.z, f.w);
+    reinterpret_cast<float4*>(p)[i] = f;
+  }
+}
 
+// Through L1: of fp32 rows a thread's 8 features are two copies of half a sector
+// each (past L1 the backward took 150 us for 107).
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// CTAs walk over batches of tokens (blockIdx.y: over the heads of a token, when
+// tokens are few).  While a batch's rows pass through, the next batch's angles
+// are computed into the other buffer, and a thread's next rows are in flight.
 template <typename T, int G, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
-    qk_norm_rope_kernel(const NormArgs a) {
-  __shared__ __align__(16) float cs[kAngles];
-  __shared__ __align__(16) float sn[kAngles];
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(const NormArgs a) {
+  __shared__ __align__(16) float cs[2][kAngles];
+  __shared__ __align__(16) float sn[2][kAngles];
   const int j = threadIdx.x % G, g = threadIdx.x / G;
   const int per_tok = (kThreads / G) >> a.tok_log2;  // groups of a token
   const int t = g / per_tok;
-  const int tok = ((int)blockIdx.x << a.tok_log2) + t;
-  const int heads = a.heads[0] + a.heads[1];
+  const int n_q = a.heads[0], heads = n_q + a.heads[1];
   const int step = per_tok * (int)gridDim.y;
-  int h = g % per_tok + per_tok * (int)blockIdx.y;
-  const bool mine = tok < a.tokens && j * 16 < a.d;
-  int o0, o1;
-  bool turned;
-  pieces<kInterleaved>(j, a.rot, o0, o1, turned);
-  constexpr int kHalf = sizeof(T) / 2;  // 16-byte words of a piece
-  auto fetch = [&](int head) {
-    Row<T> r{};
-    if (mine && head < heads) {
-      const int kind = head >= a.heads[0];
-      const T* p = static_cast<const T*>(a.x[kind]) + tok * a.x_tok[kind] +
-                   (int64_t)(head - (kind ? a.heads[0] : 0)) * a.d;
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        r.v[i] = reinterpret_cast<const uint4*>(p + o0)[i];
-        r.v[kHalf + i] = reinterpret_cast<const uint4*>(p + o1)[i];
-      }
-    }
-    return r;
-  };
-  Row<T> next = fetch(h);  // in flight while the angles are computed
-  angles(a, (int)blockIdx.x << a.tok_log2, cs, sn);
-  __syncthreads();
-  float c[8], s[8];
-  if (turned) {
-    load_angles(cs + t * (a.rot >> 1) + 8 * j, sn + t * (a.rot >> 1) + 8 * j, c, s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-  }
-  Coefs f;
-  int kind = -1;
-  const float inv_d = 1.0f / (float)a.d;
-  // Every group of the CTA takes the same number of turns: the shuffles of a
-  // warp need all its lanes.
-  const int first = per_tok * (int)blockIdx.y;
-  for (int base = first; base < heads; base += step, h += step) {
-    float x[16];
-    load8(reinterpret_cast<const T*>(&next.v[0]), x);
-    load8(reinterpret_cast<const T*>(&next.v[kHalf]), x + 8);
-    if (base + step < heads) next = fetch(h + step);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    const float r = rsqrtf(group_sum<G>(ss) * inv_d + a.eps);
-    if (mine && h < heads) {
-      const int k = h >= a.heads[0];
-      if (k != kind) {  // once for the queries, once for the keys
-        kind = k;
-        fold<kInterleaved>(a.w[k], o0, o1, c, s, f);
-      }
-      float y[16];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float u = x[kInterleaved ? 2 * i : i], v = x[kInterleaved ? 2 * i + 1 : 8 + i];
-        y[kInterleaved ? 2 * i : i] = r * (u * f.ac[i] - v * f.bs[i]);
-        y[kInterleaved ? 2 * i + 1 : 8 + i] = r * (v * f.bc[i] + u * f.as[i]);
-      }
-      T* p = static_cast<T*>(a.y[k]) + tok * a.y_tok[k] +
-             (int64_t)(h - (k ? a.heads[0] : 0)) * a.d;
-      store8(p + o0, y);
-      store8(p + o1, y + 8);
-    }
-  }
-}
-
-// Backward.  CTAs walk over batches of tokens and keep the weights' gradient
-// of their own rows in registers (fp32: a thread adds a few hundred rows at
-// most); each writes one row of sums, and the second kernel adds those in 64
-// bits.  The order depends on the sizes alone.
-template <typename T, int G, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const NormArgs a) {
-  __shared__ __align__(16) float cs[2][kAngles];
-  __shared__ __align__(16) float sn[2][kAngles];
-  __shared__ float sums[kThreads / 32][2 * 256];
-  const int j = threadIdx.x % G, g = threadIdx.x / G;
-  const int per_tok = (kThreads / G) >> a.tok_log2;
-  const int t = g / per_tok;
-  const int heads = a.heads[0] + a.heads[1];
+  const int first = per_tok * (int)blockIdx.y;  // of the CTA
+  const int h0 = first + g % per_tok;
   const bool in_row = j * 16 < a.d;
   int o0, o1;
   bool turned;
   pieces<kInterleaved>(j, a.rot, o0, o1, turned);
-  float acc[2][16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+  // Rows of head 0 of the queries, and of the keys as if they followed them.
+  const int64_t back = (int64_t)n_q * a.d;
+  const T* src0 = static_cast<const T*>(a.x[0]) + o0;
+  const T* src1 = static_cast<const T*>(a.x[1]) - back + o0;
+  T* dst0 = static_cast<T*>(a.y[0]) + o0;
+  T* dst1 = static_cast<T*>(a.y[1]) - back + o0;
+  const int apart = o1 - o0;
   const int batches = (a.tokens + (1 << a.tok_log2) - 1) >> a.tok_log2;
-  angles(a, (int)blockIdx.x << a.tok_log2, cs[0], sn[0]);
-  for (int batch = blockIdx.x, turn = 0; batch < batches; batch += gridDim.x, ++turn) {
+  const float inv_d = 1.0f / (float)a.d;
+  // The thread's own rows on their way: it copies and reads only its own 16
+  // bytes of each, so no one else has to be waited for.
+  constexpr int kWords = sizeof(T);  // 16-byte words of a thread's part of a row
+  constexpr int kDepth = 8 / kWords;
+  __shared__ uint4 ring[kDepth][kWords][kThreads];
+  int p_batch = (int)blockIdx.x, p_base = first;  // next row to ask for
+  auto push = [&](int slot) {
+    const int tok = (p_batch << a.tok_log2) + t, head = p_base + g % per_tok;
+    if (p_batch < batches && tok < a.tokens && in_row && head < heads) {
+      const T* p = (head >= n_q ? src1 + tok * a.x_tok[1] : src0 + tok * a.x_tok[0]) + head * a.d;
+#pragma unroll
+      for (int i = 0; i < kWords / 2; ++i) {
+        copy16(&ring[slot][i][threadIdx.x], reinterpret_cast<const uint4*>(p) + i);
+        copy16(&ring[slot][kWords / 2 + i][threadIdx.x],
+               reinterpret_cast<const uint4*>(p + apart) + i);
+      }
+    }
+    copy_commit();
+    p_base += step;
+    if (p_base >= heads) {
+      p_base = first;
+      p_batch += (int)gridDim.x;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) push(k);
+  int slot = 0;
+  int batch = (int)blockIdx.x;
+  angles(a, batch << a.tok_log2, cs[0], sn[0]);
+  for (int buf = 0; batch < batches; buf ^= 1) {
     const int tok = (batch << a.tok_log2) + t;
-    const int buf = turn & 1;
+    batch += (int)gridDim.x;
     __syncthreads();  // this batch's angles are there, the other buffer is free
-    if (batch + (int)gridDim.x < batches)
-      angles(a, (batch + (int)gridDim.x) << a.tok_log2, cs[buf ^ 1], sn[buf ^ 1]);
+    if (batch < batches) angles(a, batch << a.tok_log2, cs[buf ^ 1], sn[buf ^ 1]);
     float c[8], s[8];
     if (turned) {
       load_angles(cs[buf] + t * (a.rot >> 1) + 8 * j, sn[buf] + t * (a.rot >> 1) + 8 * j, c, s);
@@ -271,24 +290,158 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const Nor
 #pragma unroll
       for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
     }
+    Coefs f;
+    int kind = -1;
+    // Every group of the CTA takes the same number of turns: the shuffles of a
+    // warp need all its lanes.
+    for (int base = first, h = h0; base < heads; base += step, h += step) {
+      push(slot == 0 ? kDepth - 1 : slot - 1);
+      copy_wait<kDepth - 1>();
+      Row<T> row{};  // lanes past the row's end add nothing to its sum
+      if (in_row) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) row.v[i] = ring[slot][i][threadIdx.x];
+      }
+      if (++slot == kDepth) slot = 0;
+      uint64_t x[8];
+      unpack(row, x);
+      uint64_t sq = mul2(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
+      float lo, hi;
+      f2unpack(sq, lo, hi);
+      const float r = rsqrtf(group_sum<G>(lo + hi) * inv_d + a.eps);
+      if (tok < a.tokens && in_row && h < heads) {
+        const int k = h >= n_q;
+        if (k != kind) {  // once for the queries, once for the keys
+          kind = k;
+          fold<kInterleaved>(a.w[k], o0, o1, c, s, f);
+        }
+        const uint64_t r2 = f2pack(r, r);
+        uint64_t y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint64_t other = kInterleaved ? swapped(x[i]) : x[i ^ 4];
+          y[i] = mul2(r2, fma2(x[i], f.c[i], mul2(other, f.s[i])));
+        }
+        T* p = (k ? dst1 + tok * a.y_tok[1] : dst0 + tok * a.y_tok[0]) + h * a.d;
+        store_pairs(p, y);
+        store_pairs(p + apart, y + 4);
+      }
+    }
+  }
+}
+
+// Backward.  CTAs walk over batches of tokens as above and keep the weights'
+// gradient of their own rows in registers (fp32: a thread adds a few hundred
+// rows at most); each writes one row of sums, and the second kernel adds those
+// in 64 bits.  The order depends on the sizes alone.
+constexpr int kBwdDepth = 2;  // rows of a thread in shared memory (3: 114 us for 110)
+template <typename T>
+struct BwdSmem {
+  float cs[2][kAngles], sn[2][kAngles];
+  union {
+    uint4 ring[kBwdDepth][sizeof(T) + 4][kThreads];  // words of x, then of dy
+    float sums[kThreads / 32][2 * 256];
+  };
+};
+
+template <typename T, int G, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  BwdSmem<T>& sh = *reinterpret_cast<BwdSmem<T>*>(smem);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int j = threadIdx.x % G, g = threadIdx.x / G;
+  const int per_tok = (kThreads / G) >> a.tok_log2;
+  const int t = g / per_tok;
+  const int n_q = a.heads[0], heads = n_q + a.heads[1];
+  const bool in_row = j * 16 < a.d;
+  int o0, o1;
+  bool turned;
+  pieces<kInterleaved>(j, a.rot, o0, o1, turned);
+  const int64_t back = (int64_t)n_q * a.d;
+  const T* x0 = static_cast<const T*>(a.x[0]) + o0;
+  const T* x1 = static_cast<const T*>(a.x[1]) - back + o0;
+  const float* dy0 = a.dy[0] + o0;
+  const float* dy1 = a.dy[1] - back + o0;
+  const int apart = o1 - o0;
+  const int batches = (a.tokens + (1 << a.tok_log2) - 1) >> a.tok_log2;
+  constexpr int kWords = sizeof(T);
+  int p_batch = (int)blockIdx.x, p_head = g % per_tok;  // next row to ask for
+  auto push = [&](int slot) {
+    const int tok = (p_batch << a.tok_log2) + t;
+    if (p_batch < batches && tok < a.tokens && in_row && p_head < heads) {
+      const bool k = p_head >= n_q;
+      const T* p = (k ? x1 + tok * a.x_tok[1] : x0 + tok * a.x_tok[0]) + p_head * a.d;
+      const float* q = (k ? dy1 + tok * a.dy_tok[1] : dy0 + tok * a.dy_tok[0]) + p_head * a.d;
+#pragma unroll
+      for (int i = 0; i < kWords / 2; ++i) {
+        copy16(&sh.ring[slot][i][threadIdx.x], reinterpret_cast<const uint4*>(p) + i);
+        copy16(&sh.ring[slot][kWords / 2 + i][threadIdx.x],
+               reinterpret_cast<const uint4*>(p + apart) + i);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        copy16(&sh.ring[slot][kWords + i][threadIdx.x], reinterpret_cast<const uint4*>(q) + i);
+        copy16(&sh.ring[slot][kWords + 2 + i][threadIdx.x],
+               reinterpret_cast<const uint4*>(q + apart) + i);
+      }
+    }
+    copy_commit();
+    p_head += per_tok;
+    if (p_head - g % per_tok >= heads) {
+      p_head = g % per_tok;
+      p_batch += (int)gridDim.x;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kBwdDepth - 1; ++k) push(k);
+  int slot = 0;
+  float acc[2][16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+  angles(a, (int)blockIdx.x << a.tok_log2, sh.cs[0], sh.sn[0]);
+  int buf = 0;
+  for (int batch = blockIdx.x; batch < batches; batch += gridDim.x, buf ^= 1) {
+    const int tok = (batch << a.tok_log2) + t;
+    __syncthreads();  // this batch's angles are there, the other buffer is free
+    if (batch + (int)gridDim.x < batches)
+      angles(a, (batch + (int)gridDim.x) << a.tok_log2, sh.cs[buf ^ 1], sh.sn[buf ^ 1]);
+    float c[8], s[8];
+    if (turned) {
+      load_angles(sh.cs[buf] + t * (a.rot >> 1) + 8 * j, sh.sn[buf] + t * (a.rot >> 1) + 8 * j, c,
+                  s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    }
     const bool mine = tok < a.tokens && in_row;
     for (int base = 0; base < heads; base += per_tok) {
+      push(slot == 0 ? kBwdDepth - 1 : slot - 1);
+      copy_wait<kBwdDepth - 1>();
       const int h = base + g % per_tok;
       const bool live = mine && h < heads;
-      const int kind = h >= a.heads[0];
-      const int hk = h - (kind ? a.heads[0] : 0);
+      const int kind = h >= n_q;
       float x[16], dy[16], w[16];
       if (live) {
-        const T* p = static_cast<const T*>(a.x[kind]) + tok * a.x_tok[kind] + (int64_t)hk * a.d;
-        load8(p + o0, x);
-        load8(p + o1, x + 8);
-        const float* q = a.dy[kind] + tok * a.dy_tok[kind] + (int64_t)hk * a.d;
-        load8(q + o0, dy);
-        load8(q + o1, dy + 8);
+        Row<T> row;
+        Row<float> grad;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) row.v[i] = sh.ring[slot][i][threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) grad.v[i] = sh.ring[slot][kWords + i][threadIdx.x];
+        uint64_t p[8];
+        unpack(row, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f2unpack(p[i], x[2 * i], x[2 * i + 1]);
+        unpack(grad, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f2unpack(p[i], dy[2 * i], dy[2 * i + 1]);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = dy[i] = 0.f;
       }
+      if (++slot == kBwdDepth) slot = 0;
       if (in_row && a.w[kind]) {
         load8(a.w[kind] + o0, w);
         load8(a.w[kind] + o1, w + 8);
@@ -315,12 +468,14 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const Nor
         x[i] = r * (w[i] * dy[i] - n * m);
       }
       if (live) {
-        float* p = a.dx[kind] + ((int64_t)tok * a.heads[kind] + hk) * a.d;
+        float* p = a.dx[kind] + ((int64_t)tok * a.heads[kind] + h - (kind ? n_q : 0)) * a.d;
         store8(p + o0, x);
         store8(p + o1, x + 8);
       }
     }
   }
+  copy_wait<0>();
+  __syncthreads();  // the ring's place is taken by the sums
   // Sum over the warp's groups, then over the warps.
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -335,34 +490,39 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_bwd_kernel(const Nor
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        sums[warp][k * a.d + (i < 8 ? o0 + i : o1 + i - 8)] = acc[k][i];
+        sh.sums[warp][k * a.d + (i < 8 ? o0 + i : o1 + i - 8)] = acc[k][i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += sums[w][i];
+    for (int w = 0; w < kThreads / 32; ++w) v += sh.sums[w][i];
     a.partial[(size_t)blockIdx.x * 2 * a.d + i] = v;
   }
 }
 
-// Columns of the CTAs' sums: a block adds 32 of them, 8 rows at a time.
-__global__ void __launch_bounds__(256) qk_norm_dweight_kernel(const float* partial, int rows,
-                                                              int d, float* dwq, float* dwk) {
-  __shared__ double sh[8][32];
+// Columns of the CTAs' sums: a block adds 32 of them, 32 rows at a time.
+__global__ void __launch_bounds__(1024) qk_norm_dweight_kernel(const float* partial, int rows,
+                                                               int d, float* dwq, float* dwk) {
+  __shared__ double sh[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   double v = 0.0;
   if (col < 2 * d) {
-#pragma unroll 8
-    for (int r = y; r < rows; r += 8) v += (double)partial[(size_t)r * 2 * d + col];
+#pragma unroll 10
+    for (int r = y; r < rows; r += 32) v += (double)partial[(size_t)r * 2 * d + col];
   }
   sh[y][lane] = v;
   __syncthreads();
-  if (y == 0 && col < 2 * d) {
-    for (int i = 1; i < 8; ++i) v += sh[i][lane];
-    float* out = col < d ? dwq : dwk;
-    if (out) out[col < d ? col : col - d] = (float)v;
+  // Warp y adds column y.
+  v = sh[lane][y];
+#pragma unroll
+  for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  const int mine = blockIdx.x * 32 + y;
+  if (lane == 0 && mine < 2 * d) {
+    float* out = mine < d ? dwq : dwk;
+    if (out) out[mine < d ? mine : mine - d] = (float)v;
   }
 }
 
@@ -414,18 +574,26 @@ void dispatch(da_dtype dtype, int lanes, bool interleaved, F&& f) {
   else with_type(float{});
 }
 
-// Tokens of a CTA's batch (log2): as many as give every group of lanes a head,
-// while 148 CTAs are left; then up to four where `enough` CTAs are left, so
-// that more heads share a thread's angles.
-int batch_log2(int tokens, int heads, int lanes, int rot, int enough) {
+// Tokens of a CTA's batch (log2), for the fewest turns of the busiest CTA: a
+// batch costs ceil(heads / groups of a token) turns and about one for its
+// angles and coefficients.  More tokens share the threads of a CTA where there
+// are few heads, and let a thread use its coefficients for more rows; fewer
+// spread better over the GPU, and above `most` turns a batch nothing is gained
+// (backward, 16384 tokens of 64 heads: 1, 4, 8 turns 118, 107, 110 us; forward,
+// 40 heads: 5, 10, 20 turns 61, 57, 66 us).
+int batch_log2(int tokens, int heads, int lanes, int rot, int most) {
   const int groups = kThreads / lanes;
-  int lg = 0;
-  auto room = [&](int ctas) {
-    return (rot << lg) <= kAngles && (tokens >> (lg + 1)) >= ctas && (groups >> (lg + 1)) >= 1;
-  };
-  while (room(148) && (groups >> (lg + 1)) >= heads) ++lg;
-  while (lg < 2 && room(enough)) ++lg;
-  return lg;
+  int best = 0;
+  long long best_cost = 0;
+  for (int lg = 0; (groups >> lg) >= 1 && ((rot / 2) << lg) <= kAngles; ++lg) {
+    const int per_tok = groups >> lg;
+    const long long batches = ((long long)tokens + (1 << lg) - 1) >> lg;
+    const long long rounds = (batches + 148 * kCtasPerSm - 1) / (148 * kCtasPerSm);
+    const int turns = (heads + per_tok - 1) / per_tok;
+    const long long cost = rounds * (turns + 1);
+    if (lg == 0 || (turns <= most && cost < best_cost)) best = lg, best_cost = cost;
+  }
+  return best;
 }
 
 }  // namespace
@@ -466,12 +634,13 @@ extern "C" int diffattn_qk_norm_rope(const void* q, long long q_token_stride, co
   a.rot = rot_dim;
   a.eps = norm_eps;
   const int heads = n_q_heads + n_k_heads, lanes = da::lanes_of(head_dim);
-  a.tok_log2 = da::batch_log2(tokens, heads, lanes, rot_dim, 148 * 8);
+  a.tok_log2 = da::batch_log2(tokens, heads, lanes, rot_dim, 10);
   const int per_tok = (da::kThreads / lanes) >> a.tok_log2;
-  dim3 grid((unsigned)(((long long)tokens + (1 << a.tok_log2) - 1) >> a.tok_log2), 1, 1);
+  const long long batches = ((long long)tokens + (1 << a.tok_log2) - 1) >> a.tok_log2;
+  dim3 grid((unsigned)(batches < 148 * da::kCtasPerSm ? batches : 148 * da::kCtasPerSm), 1, 1);
   // Few tokens: a token's heads are split over CTAs too.
   const int turns = (heads + per_tok - 1) / per_tok;
-  while (grid.y < (unsigned)turns && (long long)grid.x * grid.y < 148 * 4) ++grid.y;
+  while (grid.y < (unsigned)turns && (long long)grid.x * grid.y < 148 * da::kCtasPerSm / 2) ++grid.y;
   if (grid.y > 65535u) grid.y = 65535u;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   da::dispatch(dtype, lanes, interleaved != 0, [&](auto t, auto g, auto il) {
@@ -538,18 +707,30 @@ extern "C" int diffattn_qk_norm_rope_bwd(
   a.rot = rot_dim;
   a.eps = norm_eps;
   const int heads = n_q_heads + n_k_heads, lanes = da::lanes_of(head_dim);
-  a.tok_log2 = da::batch_log2(tokens, heads, lanes, rot_dim, da::kBwdCtas);
+  a.tok_log2 = da::batch_log2(tokens, heads, lanes, rot_dim, 4);
   const int batches = (int)(((long long)tokens + (1 << a.tok_log2) - 1) >> a.tok_log2);
   const int ctas = batches < da::kBwdCtas ? batches : da::kBwdCtas;
   da::dispatch(dtype, lanes, interleaved != 0, [&](auto t, auto g, auto il) {
-    da::qk_norm_rope_bwd_kernel<decltype(t), decltype(g)::value, decltype(il)::value>
-        <<<ctas, da::kThreads, 0, cs>>>(a);
+    auto kernel = da::qk_norm_rope_bwd_kernel<decltype(t), decltype(g)::value, decltype(il)::value>;
+    constexpr int kBytes = (int)sizeof(da::BwdSmem<decltype(t)>);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) ==
+        cudaSuccess)
+      kernel<<<ctas, da::kThreads, kBytes, cs>>>(a);
   });
   if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
   if (dq_weight || dk_weight) {
-    da::qk_norm_dweight_kernel<<<(2 * head_dim + 31) / 32, 256, 0, cs>>>(
-        a.partial, ctas, head_dim, dq_weight, dk_weight);
-    if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((2 * head_dim + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = cs;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, da::qk_norm_dweight_kernel, (const float*)a.partial, ctas,
+                           head_dim, dq_weight, dk_weight) != cudaSuccess)
+      return DA_ERR_CUDA;
   }
   return DA_OK;
 }

@@ -140,14 +140,14 @@ struct Lane {
   uint32_t codes, scale;  // bytes of the tile
   uint8_t* tile;     // of KV head 0
   int64_t head_bytes;
-  // False if there is nothing to do for this lane's token.
-  __device__ __forceinline__ bool init(const CacheArgs& a) {
+  __device__ __forceinline__ Lane() {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     is_v = warp & 1;
     blk = 4 * ((warp >> 1) & 1) + (lane & 3);
     tok = (int)blockIdx.x * kTokens + 8 * (warp >> 2) + (lane >> 2);
-    if (tok >= a.tokens) return false;
-    const int slot = a.slots[tok];
+  }
+  // Where the token is held; false if there is nothing to do for it.
+  __device__ __forceinline__ bool find(const CacheArgs& a, int slot) {
     if (slot < 0) return false;
     if (slot >= a.n_slots) {
       report(a.dev_status, DA_ERR_PAGE);
@@ -170,11 +170,13 @@ struct Lane {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a) {
   Lane w;
-  if (!w.init(a)) return;
+  if (w.tok >= a.tokens) return;
   const T* src = (w.is_v ? static_cast<const T*>(a.v) + w.tok * a.v_tok
                          : static_cast<const T*>(a.k) + w.tok * a.k_tok) + w.blk * 16;
+  const int slot = a.slots[w.tok];
   int h = blockIdx.y;
-  Block<T> next = load_block(src + (int64_t)h * kKv4Row);
+  Block<T> next = load_block(src + (int64_t)h * kKv4Row);  // not held up by the slot
+  if (!w.find(a, slot)) return;
   for (; h < a.heads; h += gridDim.y) {
     const Block<T> b = next;
     if (h + (int)gridDim.y < a.heads)
@@ -230,30 +232,38 @@ __device__ __forceinline__ void store_block(__nv_bfloat16* p, const uint32_t (&h
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
+  constexpr int kAtOnce = 4;  // heads asked for together
   Lane w;
-  if (!w.init(a)) return;
+  if (w.tok >= a.tokens || !w.find(a, a.slots[w.tok])) return;
   T* dst = static_cast<T*>(w.is_v ? a.v_out : a.k_out) + (int64_t)w.tok * a.heads * kKv4Row +
            w.blk * 16;
-  int h = blockIdx.y;
-  auto fetch = [&](int head, uint2& c, uint32_t& sb) {
-    const uint8_t* tile = w.tile + head * w.head_bytes;
-    c = *reinterpret_cast<const uint2*>(tile + w.codes);
-    sb = tile[w.scale];
-  };
-  uint2 c_next;
-  uint32_t s_next;
-  fetch(h, c_next, s_next);
-  for (; h < a.heads; h += gridDim.y) {
-    const uint2 c = c_next;
-    const uint32_t s = (s_next << 7) * 0x10001u;  // the scale twice, fp16
-    if (h + (int)gridDim.y < a.heads) fetch(h + gridDim.y, c_next, s_next);
-    uint32_t x[8];
-    e2m1x8_to_f16x2(c.x, x[0], x[1], x[2], x[3]);
-    e2m1x8_to_f16x2(c.y, x[4], x[5], x[6], x[7]);
+  const int step = (int)gridDim.y;
+  for (int h0 = blockIdx.y; h0 < a.heads; h0 += kAtOnce * step) {
+    uint2 c[kAtOnce];
+    uint32_t s[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // exact in fp16
-      asm("mul.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(s));
-    store_block<kWide>(dst + (int64_t)h * kKv4Row, x);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int h = h0 + k * step;
+      c[k] = make_uint2(0u, 0u), s[k] = 0u;
+      if (h < a.heads) {
+        const uint8_t* tile = w.tile + h * w.head_bytes;
+        c[k] = __ldg(reinterpret_cast<const uint2*>(tile + w.codes));
+        s[k] = __ldg(tile + w.scale);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int h = h0 + k * step;
+      if (h >= a.heads) break;
+      const uint32_t s2 = (s[k] << 7) * 0x10001u;  // the scale twice, fp16
+      uint32_t x[8];
+      e2m1x8_to_f16x2(c[k].x, x[0], x[1], x[2], x[3]);
+      e2m1x8_to_f16x2(c[k].y, x[4], x[5], x[6], x[7]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // exact in fp16
+        asm("mul.f16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(s2));
+      store_block<kWide>(dst + (int64_t)h * kKv4Row, x);
+    }
   }
 }
 

@@ -71,6 +71,7 @@ struct Kv4Args {
   int cols;     // columns kept per slot
   float* part_o;   // [slot][cols][128]
   float* part_ml;  // [slot][cols][2]
+  int2* spans;     // [batch][units]: first run and segments of a unit, or null
   int* dev_status;
   // combine
   const float* lambda;
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       }
       const uint32_t have = loaded[slot];
       const int first_tok = (s0 + i) * kStageTokens;
-      const bool part = have != 15u || first_tok < lo || first_tok + kStageTokens > len;
+      const bool part = have != 15u || first_tok < lo || len - first_tok < kStageTokens;
 #pragma unroll
       for (int pair = 0; pair < kTiles / 2; ++pair) {
         const uint32_t at = ring_at + slot * kStageBytes + pair * 2 * kKv4TileBytes;
@@ -567,6 +568,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       if (++slot == kRing) slot = 0, parity ^= 1u;
     }
 
+    if (a.spans && s_first == 0 && lane == 0) {
+      const long long last = pos + n_b - 1;  // of the unit
+      a.spans[(size_t)b * units + unit] = make_int2(me, (int)divide(last, run) - me + 1);
+    }
     // The segment's sums.  Slots are ordered as the segments are: the next
     // segment has the next unit or the next run.
     const long long part = (long long)b * units + unit + me;
@@ -624,12 +629,20 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
   }
   const int units = a.heads * a.chunks;
   const int n_b = stages_of(a, b);
-  long long before, total;
-  stage_sums(a, b, before, total);
-  const long long run = run_length(a, total * units);
-  const long long start = before * units + (long long)unit * n_b;
-  const int w0 = (int)divide(start, run);
-  const int n = n_b > 0 ? (int)divide(start + n_b - 1, run) - w0 + 1 : 0;
+  int w0 = 0, n = 0;  // first run, and segments
+  if (!a.spans) {
+    long long before, total;
+    stage_sums(a, b, before, total);
+    const long long run = run_length(a, total * units);
+    const long long start = before * units + (long long)unit * n_b;
+    w0 = (int)divide(start, run);
+    n = n_b > 0 ? (int)divide(start + n_b - 1, run) - w0 + 1 : 0;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.spans && n_b > 0) {
+    const int2 v = a.spans[(size_t)b * units + unit];
+    w0 = v.x, n = v.y;
+  }
   const long long slot0 = (long long)b * units + unit + w0;
   const float* ml = a.part_ml + (slot0 * a.cols + col) * 2;
   const float* po = a.part_o + (slot0 * a.cols + col) * kD + 4 * lane;
@@ -638,7 +651,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
   float gain[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) gain[i] = a.gain ? a.gain[4 * lane + i] : 1.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, o[2][4] = {};
   for (int s0 = warp; s0 < n; s0 += kCombineWarps * kAtOnce) {
     float4 v[kAtOnce], x[kAtOnce], y[kAtOnce];
@@ -710,9 +722,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 constexpr int kRuns = kPlanSms * kCtasPerSm * kWarps;
 
+// Up to this many sequences the second kernel finds a unit's segments by adding
+// up the lengths before it, which costs no trip to what the first kernel wrote
+// (one trip, 0.6 us, of 8 for two short requests); above, where every CTA's
+// sums would cost the square of the batch, the first kernel writes them down.
+constexpr int kSumBatch = 256;
+
 size_t workspace_bytes_of(int batch, int units, int cols) {
   const size_t slots = (size_t)batch * units + kRuns;
-  return slots * cols * (kD + 2) * sizeof(float);
+  return slots * cols * (kD + 2) * sizeof(float) +
+         (batch > kSumBatch ? (size_t)batch * units * sizeof(int2) : 0);
 }
 
 int chunks_of(int group) { return (group + kChunkHeads - 1) / kChunkHeads; }
@@ -722,6 +741,7 @@ cudaError_t launch(Kv4Args& a, void* workspace, cudaStream_t stream) {
   const size_t slots = (size_t)a.batch * a.heads * a.chunks + a.runs;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + slots * a.cols * kD;
+  a.spans = a.batch > kSumBatch ? reinterpret_cast<int2*>(a.part_ml + slots * a.cols * 2) : nullptr;
   const unsigned grid = (unsigned)(a.runs / kWarps);
   auto run = [&](auto kernel) -> cudaError_t {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

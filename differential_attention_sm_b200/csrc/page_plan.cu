@@ -73,8 +73,13 @@ __device__ long long block_scan(long long x, long long* sh, long long& total) {
   return x + (warp ? sh[warp - 1] : 0);
 }
 
-__device__ __forceinline__ int slot_of(int page, int pos, int shift) {
-  return (int)(((unsigned)page << shift) + (unsigned)(pos & ((1 << shift) - 1)));
+// Slot of a position on a page; -1, and `bad` set, if it is no page.
+__device__ __forceinline__ int slot_of(const PlanArgs& a, int page, int pos, bool& bad) {
+  if ((unsigned)page >= (unsigned)a.n_pages) {
+    bad = true;
+    return -1;
+  }
+  return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
 // `with_slots`: this launch writes the slot rows and table entries too.
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
   const long long room = (long long)a.max_pages << a.page_shift;
   long long tok_base = 0, need_base = 0;
   int taken = 0;         // the most pages that a served request reaches down to
-  bool refused = false;
+  bool refused = false, bad = false;
   for (int base = 0; base < a.requests; base += (int)blockDim.x) {
     const int r = base + tid;
     const bool live = r < a.requests;
@@ -128,8 +133,8 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
         const int pos = (int)((unsigned)len + (unsigned)j), blk = pos >> a.page_shift;
         int slot = -1;
         if (ok)
-          slot = slot_of(blk < old ? row[blk] : a.stack[free0 - 1 - (depth + blk - old)], pos,
-                         a.page_shift);
+          slot = slot_of(a, blk < old ? row[blk] : a.stack[free0 - 1 - (depth + blk - old)], pos,
+                         bad);
         a.slots[tok_at + j] = slot;
         a.positions[tok_at + j] = pos;
       }
@@ -153,8 +158,8 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
         int slot = -1;
         if (w_ok)
           slot = slot_of(
-              blk < w_old ? w_row[blk] : a.stack[free0 - 1 - (w_depth + blk - w_old)], pos,
-              a.page_shift);
+              a, blk < w_old ? w_row[blk] : a.stack[free0 - 1 - (w_depth + blk - w_old)], pos,
+              bad);
         a.slots[w_at + j] = slot;
         a.positions[w_at + j] = pos;
       }
@@ -178,6 +183,7 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
     for (int w = 1; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, top[w]);
     *a.count_out = free0 - taken;
   }
+  if (bad) report(a.dev_status, DA_ERR_PAGE);
   if (refused) report(a.dev_status, DA_ERR_CACHE_FULL);
 }
 
@@ -227,6 +233,7 @@ __global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs
   __syncthreads();
   const int total = a.offsets[a.requests];
   const int mask = (1 << a.page_shift) - 1;
+  bool bad = false;
   for (int i = first + threadIdx.x; i <= last; i += kFillThreads) {
     int slot = -1, pos = 0;
     if (i < total) {
@@ -245,12 +252,13 @@ __global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs
           page = a.stack[q.depth - 1 - (blk - old)];
           if ((pos & mask) == 0) *entry = page;
         }
-        slot = slot_of(page, pos, a.page_shift);
+        slot = slot_of(a, page, pos, bad);
       }
     }
     a.slots[i] = slot;
     a.positions[i] = pos;
   }
+  if (bad) report(a.dev_status, DA_ERR_PAGE);
 }
 
 // Pages of the released requests go back on the stack in request order.

@@ -542,7 +542,7 @@ int check(const void* q, const void* k, long long q_tok, long long k_tok, da_dty
   if (tokens < 0 || n_q < 1 || n_k < 0 || d < 1 || rot < 0 || rot > d) return DA_ERR_INVALID_ARG;
   if (!(eps >= 0.f)) return DA_ERR_INVALID_ARG;
   if (d % 16 || d > 256 || rot % 16) return DA_ERR_UNSUPPORTED;
-  if (n_q > (1 << 20) || n_k > (1 << 20)) return DA_ERR_UNSUPPORTED;
+  if (tokens > (1 << 30) || n_q > (1 << 20) || n_k > (1 << 20)) return DA_ERR_UNSUPPORTED;
   if (tokens == 0) return DA_OK;
   if (!q || (n_k > 0 && !k) || (rot > 0 && (!positions || !inv_freq))) return DA_ERR_INVALID_ARG;
   if (q_tok < (long long)n_q * d || (n_k > 0 && k_tok < (long long)n_k * d))

@@ -470,8 +470,9 @@ DA_API size_t diffattn_kv4_page_bytes(int n_kv_heads, int head_dim, int page_siz
  * All device pointers.  slots and positions may be NULL with n_slots = 0.
  *   workspace     : device scratch of the queried size (0 for up to 1024 slot
  *                   rows; workspace may be NULL then)
- * Up to 65536 requests and 2^30 slot rows.  DA_ERR_CACHE_FULL goes to dev_status if a request
- * was not served.  The result depends on the arguments' values alone, and a
+ * Up to 65536 requests and 2^30 slot rows.  DA_ERR_CACHE_FULL goes to
+ * dev_status if a request was not served, DA_ERR_PAGE if a token would lie on
+ * a page out of range (its slot is -1).  The result depends on the arguments' values alone, and a
  * call repeated with the same ones writes the same. */
 DA_API size_t diffattn_page_plan_workspace_size(int requests, int n_slots);
 DA_API int diffattn_page_plan(const int* new_lens, const int* cache_lens, int* block_table,
@@ -554,7 +555,8 @@ DA_API int diffattn_v1_decode_kv4(const void* q, const void* cache, int n_pages,
  *   positions   : device int32 [tokens]; inv_freq: device fp32 [rot_dim / 2];
  *                 both may be NULL with rot_dim = 0 (norm only)
  * Angles are formed in 64 bits.  head_dim and rot_dim multiples of 16,
- * head_dim <= 256 (DA_ERR_UNSUPPORTED otherwise). */
+ * head_dim <= 256, at most 2^30 tokens and 2^20 heads of each kind
+ * (DA_ERR_UNSUPPORTED otherwise). */
 DA_API int diffattn_qk_norm_rope(const void* q, long long q_token_stride, const void* k,
                                  long long k_token_stride, da_dtype dtype, int tokens,
                                  int n_q_heads, int n_k_heads, int head_dim,

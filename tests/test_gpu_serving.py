@@ -122,6 +122,19 @@ def test_page_plan_limits(B):
     assert np.array_equal(t.cpu().numpy(), ref["block_table"])
 
 
+@pytest.mark.parametrize("slots", [20, 6000])
+def test_page_plan_pages_out_of_range(B, slots):
+    """Entries that are no page give no slot and are reported."""
+    table = np.array([[1 << 30, -1], [2, -1], [-1, -1]])
+    st = status_word()
+    t = dev(table, I32)
+    got = B.diffattn_page_plan(dev([1, 1, 17], I32), dev([3, 3, 0], I32), t,
+                               dev([0, 77, 1], I32), dev([3], I32), 16, slots, dev_status=st)
+    assert list(got["slots"].cpu()[:19]) == [-1, 2 * 16 + 3] + list(range(16, 32)) + [-1]
+    assert list(t.cpu()[2]) == [1, 77] and int(st.item()) == B.DA_ERR_PAGE
+    assert int(got["free_count"].item()) == 1 and list(got["served"].cpu()) == [1, 1, 1]
+
+
 @pytest.mark.parametrize("requests,page", [(1, 16), (37, 64), (1300, 16)])
 def test_page_release(B, requests, page):
     new, lens, table, stack, free = plan_state(3, requests, page, 40 * page, 0, 1.0)
@@ -491,11 +504,12 @@ def test_v1_decode(B, lens, H, page, window, norm):
                  (1e-5, 1 + 0.2 * rng.standard_normal(128), 0.7) if norm else None)
 
 
-def test_decode_many_short_sequences(B):
-    """More sequences than warps: runs that cross many sequences."""
+@pytest.mark.parametrize("Bn,longest", [(700, 70), (256, 300), (257, 300)])
+def test_decode_many_short_sequences(B, Bn, longest):
+    """Runs that cross many sequences; both ways to find a unit's segments."""
     rng = np.random.default_rng(8)
-    lens = list(rng.integers(0, 70, 700))
-    cache, table, q, rng = decode_state(700, lens, 2, 16, 4, seed=3)
+    lens = list(rng.integers(0, longest, Bn))
+    cache, table, q, rng = decode_state(Bn, lens, 2, 16, 4, seed=3)
     check_decode(B, cache, table, lens, q, rng.uniform(0, 1, 2), 2)
 
 

@@ -651,9 +651,10 @@ def diffattn_selftest_wait_timeout(timeout_us, dev_status, waited_ns=None, strea
 
 
 # ---- serving: page plan, 4-bit paged cache, decode over it; QK norm + rotation
-# These calls take microseconds on the GPU, so the checks here are the cheap
-# forms: one comparison each, device indices instead of device objects, and the
-# device is only switched when it is not the current one.
+# These calls take microseconds on the GPU, as long as a few checks take here.
+# So each call first asks in one expression whether all is as it should be, and
+# only otherwise goes through the named checks, which say what is not; devices
+# are compared by index, and switched only when the device is not the current.
 _I32, _U8, _F32, _BF16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
 _CODES = {_BF16: DA_BF16, _F32: DA_FP32}
 
@@ -679,10 +680,9 @@ def _one_device(first, *others):
     return at
 
 
-def _run(name, at, stream, *args):
+def _run(fn, at, stream, *args):
     """Calls an entry point with device `at` current, on `stream` (None: that
     device's current stream)."""
-    fn = getattr(load(), name)
     if torch._C._cuda_getDevice() != at:
         with torch.cuda.device(at):
             status = fn(*args, _stream(stream))
@@ -690,7 +690,7 @@ def _run(name, at, stream, *args):
         status = fn(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None
                     else _stream(stream))
     if status != DA_OK:
-        raise DiffAttnError(name, status)
+        raise DiffAttnError(fn.__name__, status)
 
 
 def _token_stride(name, t, tokens=None, dtype=None):
@@ -726,17 +726,29 @@ def _workspace(workspace, need, at, stream):
 
 def _kv4_cache(cache):
     """(pages, KV heads, page size) of a cache [n_pages, n_kv_heads, page_size * 144]."""
-    _need("cache", cache, _U8)
-    if cache.dim() != 3 or cache.shape[2] % 144:
-        raise ValueError("cache must be [n_pages, n_kv_heads, page_size * 144], not %s"
-                         % (tuple(cache.shape),))
-    pages, heads, nbytes = cache.shape
-    return pages, heads, nbytes // 144
+    if cache.dtype is not _U8 or not cache.is_contiguous():
+        _need("cache", cache, _U8)
+    if cache.dim() == 3:
+        pages, heads, nbytes = cache.shape
+        if nbytes % 144 == 0:
+            return pages, heads, nbytes // 144
+    raise ValueError("cache must be [n_pages, n_kv_heads, page_size * 144], not %s"
+                     % (tuple(cache.shape),))
 
 
 def _page_lists(first, cache_lens, block_table, free_pages, free_count):
     """(requests, max_pages, n_pages), all checked."""
     R = first.numel()
+    if (first.dtype is _I32 and cache_lens.dtype is _I32 and block_table.dtype is _I32 and
+            free_pages.dtype is _I32 and free_count.dtype is _I32 and first.is_contiguous() and
+            cache_lens.is_contiguous() and block_table.is_contiguous() and
+            free_pages.is_contiguous() and free_count.numel() == 1 and
+            first.dim() == cache_lens.dim() == free_pages.dim() == free_count.dim() == 1 and
+            cache_lens.numel() == R and block_table.dim() == 2):
+        rows, max_pages = block_table.shape
+        if rows == R:
+            return R, max_pages, free_pages.numel()
+    _need("new_lens or release", first, _I32, (R,))
     _need("cache_lens", cache_lens, _I32, (R,))
     _need("block_table", block_table, _I32)
     _need("free_pages", free_pages, _I32)
@@ -763,7 +775,6 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
     dict, is written instead of new tensors; its cache_lens and free_count
     may be the arguments themselves."""
     R, max_pages, n_pages = _page_lists(new_lens, cache_lens, block_table, free_pages, free_count)
-    _need("new_lens", new_lens, _I32, (R,))
     if n_slots < 0:
         raise ValueError("n_slots is negative")
     need = 0
@@ -786,7 +797,7 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
                          dev_status, slots, positions, offsets, served, lens, count)
     if need:
         workspace = _workspace(None, need, at, stream)
-    _run("diffattn_page_plan", at, stream, new_lens.data_ptr(), cache_lens.data_ptr(),
+    _run((_lib or load()).diffattn_page_plan, at, stream, new_lens.data_ptr(), cache_lens.data_ptr(),
          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
          n_pages, page_size, n_slots, slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
          served.data_ptr(), lens.data_ptr(), count.data_ptr(), _ptr(workspace),
@@ -799,9 +810,8 @@ def diffattn_page_release(release, cache_lens, block_table, free_pages, free_cou
     """Gives the pages of requests with release[r] != 0 back (int32 [R]);
     cache_lens, block_table, free_pages and free_count are changed in place."""
     R, max_pages, n_pages = _page_lists(release, cache_lens, block_table, free_pages, free_count)
-    _need("release", release, _I32, (R,))
     at = _one_device(release, cache_lens, block_table, free_pages, free_count, dev_status)
-    _run("diffattn_page_release", at, stream, release.data_ptr(), cache_lens.data_ptr(),
+    _run((_lib or load()).diffattn_page_release, at, stream, release.data_ptr(), cache_lens.data_ptr(),
          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
          n_pages, page_size, _ptr(dev_status))
 
@@ -819,12 +829,13 @@ def diffattn_kv4_append(k, v, slots, cache, *, dev_status=None, stream=None):
     dtype = _code("k", k)
     ks, vs = _token_stride("k", k), _token_stride("v", v, None, k.dtype)
     T, H, d = k.shape
-    _need("slots", slots, _I32, (T,))
+    if slots.dtype is not _I32 or slots.shape != (T,) or not slots.is_contiguous():
+        _need("slots", slots, _I32, (T,))
     pages, heads, ps = _kv4_cache(cache)
     if heads != H:
         raise ValueError("cache holds %d heads, k %d" % (heads, H))
     at = _one_device(k, v, slots, cache, dev_status)
-    _run("diffattn_kv4_append", at, stream, k.data_ptr(), ks, v.data_ptr(), vs, dtype,
+    _run((_lib or load()).diffattn_kv4_append, at, stream, k.data_ptr(), ks, v.data_ptr(), vs, dtype,
          slots.data_ptr(), T, H, d, cache.data_ptr(), pages, ps, _ptr(dev_status))
     return cache
 
@@ -834,18 +845,20 @@ def diffattn_kv4_read(cache, slots, *, out=None, dtype=torch.bfloat16, dev_statu
     """Rows (k, v) [T, Hkv, 128] held at slots int32 [T].  Rows of negative
     slots are left as they were in `out` = (k, v), or are 0 in new tensors."""
     pages, H, ps = _kv4_cache(cache)
-    _need("slots", slots, _I32)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [tokens]")
+    if slots.dtype is not _I32 or slots.dim() != 1 or not slots.is_contiguous():
+        _need("slots", slots, _I32, (slots.numel(),))
     T = slots.shape[0]
     if out is None:
         out = tuple(torch.zeros(T, H, 128, dtype=dtype, device=cache.device) for _ in "kv")
     k, v = out
     code = _code("k", k)
-    _need("k", k, k.dtype, (T, H, 128))
-    _need("v", v, k.dtype, (T, H, 128))
+    shape = (T, H, 128)
+    if (v.dtype is not k.dtype or k.shape != shape or v.shape != shape or
+            not k.is_contiguous() or not v.is_contiguous()):
+        _need("k", k, k.dtype, shape)
+        _need("v", v, k.dtype, shape)
     at = _one_device(cache, slots, k, v, dev_status)
-    _run("diffattn_kv4_read", at, stream, cache.data_ptr(), pages, ps, slots.data_ptr(), T, H, 128,
+    _run((_lib or load()).diffattn_kv4_read, at, stream, cache.data_ptr(), pages, ps, slots.data_ptr(), T, H, 128,
          k.data_ptr(), v.data_ptr(), code, _ptr(dev_status))
     return k, v
 
@@ -871,7 +884,7 @@ def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
         _need("out", out, q.dtype, (B, Hq // 2, d))
     ws = _workspace(workspace, 0 if workspace is not None else
                     diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv), at, stream)
-    _run("diffattn_v2_decode_kv4", at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
+    _run((_lib or load()).diffattn_v2_decode_kv4, at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
          block_table.data_ptr(), max_pages, cache_lens.data_ptr(), window, out.data_ptr(), code, B,
          Hq, Hkv, d, lam.data_ptr(), ws.data_ptr(), ws.nbytes, _ptr(dev_status))
     return out
@@ -879,12 +892,16 @@ def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
 
 def _decode_lists(B, block_table, cache_lens, lam, n_lam):
     """max_pages of a decode's tables, all checked."""
-    _need("block_table", block_table, _I32)
+    if (block_table.dtype is not _I32 or cache_lens.dtype is not _I32 or lam.dtype is not _F32 or
+            cache_lens.shape != (B,) or lam.shape != (n_lam,) or
+            not block_table.is_contiguous() or not cache_lens.is_contiguous() or
+            not lam.is_contiguous()):
+        _need("block_table", block_table, _I32)
+        _need("cache_lens", cache_lens, _I32, (B,))
+        _need("lam", lam, _F32, (n_lam,))
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [%d, max_pages], not %s"
                          % (B, tuple(block_table.shape)))
-    _need("cache_lens", cache_lens, _I32, (B,))
-    _need("lam", lam, _F32, (n_lam,))
     return block_table.shape[1]
 
 
@@ -914,7 +931,7 @@ def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
         _need("out", out, q.dtype, (B, H, 128))
     ws = _workspace(workspace, 0 if workspace is not None else
                     diffattn_v1_decode_kv4_workspace_size(B, H), at, stream)
-    _run("diffattn_v1_decode_kv4", at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
+    _run((_lib or load()).diffattn_v1_decode_kv4, at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
          block_table.data_ptr(), max_pages, cache_lens.data_ptr(), window, out.data_ptr(), code, B,
          H, d2 // 2, 128, lam.data_ptr(), int(bool(apply_norm)), _ptr(norm_weight), norm_eps,
          lambda_init, ws.data_ptr(), ws.nbytes, _ptr(dev_status))
@@ -922,24 +939,34 @@ def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
 
 
 def _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight):
+    dtype = q.dtype
     code = _code("q", q)
-    qs = _token_stride("q", q)
     T, Hq, d = q.shape
-    Hk, ks = 0, 0
+    qs, sh, sd = q.stride()
+    if sd != 1 or sh != d or T < 2:
+        qs = _token_stride("q", q)
+    Hk = ks = 0
     if k is not None:
-        ks = _token_stride("k", k, T, q.dtype)
-        Hk = k.shape[1]
-        if k.shape[2] != d:
+        Tk, Hk, dk = k.shape
+        ks, sh, sd = k.stride()
+        if sd != 1 or sh != d or Tk != T or T < 2 or k.dtype is not dtype:
+            ks = _token_stride("k", k, T, dtype)
+        if dk != d:
             raise ValueError("q and k differ in width")
-    if q_weight is not None:
+    if q_weight is not None and (q_weight.dtype is not _F32 or q_weight.shape != (d,) or
+                                 not q_weight.is_contiguous()):
         _need("q_weight", q_weight, _F32, (d,))
-    if k_weight is not None:
+    if k_weight is not None and (k_weight.dtype is not _F32 or k_weight.shape != (d,) or
+                                 not k_weight.is_contiguous()):
         _need("k_weight", k_weight, _F32, (d,))
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _need("inv_freq", inv_freq, _F32, (rot // 2,))
-    if positions is not None:
+        if (inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or
+                not inv_freq.is_contiguous()):
+            _need("inv_freq", inv_freq, _F32, (rot // 2,))
+    if positions is not None and (positions.dtype is not _I32 or positions.shape != (T,) or
+                                  not positions.is_contiguous()):
         _need("positions", positions, _I32, (T,))
     return code, T, Hq, Hk, d, qs, ks, rot
 
@@ -968,7 +995,7 @@ def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=
         if k is not None:
             kos = _token_stride("k out", ko, T, q.dtype)
         at = _one_device(q, k, positions, inv_freq, q_weight, k_weight, qo, ko)
-    _run("diffattn_qk_norm_rope", at, stream, q.data_ptr(), qs, _ptr(k), ks, code, T, Hq, Hk, d,
+    _run((_lib or load()).diffattn_qk_norm_rope, at, stream, q.data_ptr(), qs, _ptr(k), ks, code, T, Hq, Hk, d,
          _ptr(q_weight), _ptr(k_weight), norm_eps, _ptr(positions), _ptr(inv_freq), rot,
          int(bool(interleaved)), qo.data_ptr(), qos, _ptr(ko), kos)
     return qo, ko
@@ -989,15 +1016,23 @@ def diffattn_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, *, q_we
                                                       k_weight)
     if dq_out.shape != q.shape or (k is not None and dk_out.shape != k.shape):
         raise ValueError("the gradients must have the inputs' shapes")
-    gqs = _token_stride("dq_out", dq_out, T, _F32)
-    gks = 0 if k is None else _token_stride("dk_out", dk_out, T, _F32)
+    if dq_out.dtype is _F32 and dq_out.is_contiguous():
+        gqs = Hq * d
+    else:
+        gqs = _token_stride("dq_out", dq_out, T, _F32)
+    if k is None:
+        gks = 0
+    elif dk_out.dtype is _F32 and dk_out.is_contiguous():
+        gks = Hk * d
+    else:
+        gks = _token_stride("dk_out", dk_out, T, _F32)
     at = _one_device(q, k, dq_out, dk_out, positions, inv_freq, q_weight, k_weight, workspace)
     r = {"dq": torch.empty_like(dq_out), "dk": None if k is None else torch.empty_like(dk_out),
          "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
          "dk_weight": None if k is None or k_weight is None else torch.empty_like(k_weight)}
     ws = _workspace(workspace, 0 if workspace is not None else
                     diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), at, stream)
-    _run("diffattn_qk_norm_rope_bwd", at, stream, q.data_ptr(), qs, _ptr(k), ks, code,
+    _run((_lib or load()).diffattn_qk_norm_rope_bwd, at, stream, q.data_ptr(), qs, _ptr(k), ks, code,
          dq_out.data_ptr(), gqs, _ptr(dk_out), gks, T, Hq, Hk, d, _ptr(q_weight), _ptr(k_weight),
          norm_eps, _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
          r["dq"].data_ptr(), _ptr(r["dk"]), _ptr(r["dq_weight"]), _ptr(r["dk_weight"]),

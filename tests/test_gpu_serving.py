@@ -548,6 +548,49 @@ def test_decode_nan_block_and_pages_out_of_range(B):
     within(got[1], ref, bound + 2.0 ** -8 * np.abs(ref), "without bad pages")
 
 
+def test_decode_masked_places_hold_anything(B):
+    """NaN blocks before the window's first token, in its tile and its stage;
+    queries of zeros, whose weights are even."""
+    lens, window = [200, 77], 60
+    cache, table, q, rng = decode_state(2, lens, 1, 16, 4, seed=23)
+    clean = cache.copy()
+    tiles = cache.reshape(len(cache), 1, -1, 2304)
+    for b, n in enumerate(lens):
+        for t in range(n - window):
+            for kind in "kv":
+                for ch in range(0, 128, 16):
+                    tiles[table[b, t // 16], 0, 0, R.byte_of(kind, t % 16, ch)[1]] = 0xFF
+    q[0, 2] = 0
+    q[1, 1] = 0
+    out = check_decode(B, cache, table, lens, q, [0.4, -0.3], 2, window)
+    assert torch.equal(out, check_decode(B, clean, table, lens, q, [0.4, -0.3], 2, window))
+
+
+def test_cache_beyond_32_bits(B):
+    """Pages whose bytes lie past 2^32: appended, read and attended to there as
+    in a small cache."""
+    pages, H, ps, n = 150000, 16, 16, 70
+    cache = torch.empty(pages, H, ps * 144, dtype=torch.uint8, device="cuda")
+    assert cache.numel() > 5 * 2 ** 30
+    small = torch.zeros(5, H, ps * 144, dtype=torch.uint8, device="cuda")
+    at = torch.tensor([pages - 1, 3, pages - 77, 120000, pages // 2], dtype=I32, device="cuda")
+    near = torch.arange(5, dtype=I32, device="cuda")
+    pos = torch.arange(n, device="cuda")
+    slots = [(t[pos // ps] * ps + pos % ps).to(I32) for t in (at, near)]
+    k, v = (torch.randn(n, H, 128, device="cuda").to(torch.bfloat16) for _ in "kv")
+    for c, sl in zip((cache, small), slots):
+        B.diffattn_kv4_append(k, v, sl, c)
+    assert torch.equal(cache[at.long(), :, :64 * 16], small[:, :, :64 * 16])
+    got, want = B.diffattn_kv4_read(cache, slots[0]), B.diffattn_kv4_read(small, slots[1])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q = torch.randn(1, 4 * H, 128, device="cuda").to(torch.bfloat16)
+    lam = torch.rand(2 * H, device="cuda")
+    ln = torch.tensor([n], dtype=I32, device="cuda")
+    a = B.diffattn_v2_decode_kv4(q, cache, at[None].contiguous(), ln, lam)
+    b = B.diffattn_v2_decode_kv4(q, small, near[None].contiguous(), ln, lam)
+    assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
 def test_decode_lengths_are_clamped(B):
     lens = [64, 32]
     cache, table, q, rng = decode_state(2, lens, 1, 16, 2, seed=22)
@@ -656,6 +699,86 @@ def test_serving_steps(B):
                 K = V = np.zeros((Hkv, 0, 128))
             o, bound = R.decode(np64(q[r]), K, V, lam_h.astype(np.float64), 2)
             within(out[r], o, bound + 2.0 ** -8 * np.abs(o), "step %d request %d" % (step, r))
+
+
+def test_step_as_a_graph(B):
+    """A whole step captured once and replayed with other lengths, against the
+    same calls made one by one."""
+    Rn, H, page, n_pages, T = 3, 2, 16, 40, 24
+    i32 = dict(dtype=I32, device="cuda")
+
+    def state():
+        return dict(new=torch.ones(Rn, **i32), lens=torch.zeros(Rn, **i32),
+                    table=torch.full((Rn, 10), -1, **i32), stack=torch.arange(n_pages, **i32),
+                    count=torch.full((1,), n_pages, **i32),
+                    cache=torch.zeros(n_pages, H, page * 144, dtype=torch.uint8, device="cuda"))
+
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(T, 8 * 128, generator=g).to(torch.bfloat16).cuda()
+    f = (10000.0 ** (-torch.arange(0, 128, 2, dtype=torch.float64) / 128)).float().cuda()
+    w, lam = torch.ones(128, device="cuda"), torch.tensor([0.2, 0.7], device="cuda")
+    ws = torch.empty(B.diffattn_v2_decode_kv4_workspace_size(Rn, 4, H), dtype=torch.uint8,
+                     device="cuda")
+
+    def step(s):
+        q, k, v = (t.unflatten(1, (-1, 128)) for t in x.split([512, 256, 256], 1))
+        p = B.diffattn_page_plan(s["new"], s["lens"], s["table"], s["stack"], s["count"], page, T)
+        q, k = B.diffattn_qk_norm_rope(q, k, p["positions"], f, q_weight=w, k_weight=w)
+        B.diffattn_kv4_append(k, v, p["slots"], s["cache"])
+        last = (p["offsets"][1:] - 1).clamp(min=0).long()
+        out = B.diffattn_v2_decode_kv4(q[last], s["cache"], s["table"], p["cache_lens"], lam,
+                                       workspace=ws)
+        s["lens"].copy_(p["cache_lens"])
+        s["count"].copy_(p["free_count"])
+        return out
+
+    a, b = state(), state()
+    step(b)                       # warm-up, on a state that is then put back
+    fresh = state()
+    for name in b:
+        b[name].copy_(fresh[name])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(b)
+    for new in ([5, 17, 1], [1, 1, 1], [1, 0, 16], [2, 9, 1]):
+        for s in (a, b):
+            s["new"].copy_(torch.tensor(new, dtype=I32))
+        want = step(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        for name in a:
+            assert torch.equal(a[name], b[name]), name
+
+
+def test_norm_backward_as_a_graph(B):
+    s = norm_state(300, 6, 2, 128, 128, torch.bfloat16, True, True, 5000)
+    dy = [torch.randn(300, H, 128, generator=s["g"]).cuda() for H in (6, 2)]
+    args = (s["qd"], s["kd"], *dy, cu(s["pos"]), cu(s["f"]))
+    kw = dict(q_weight=cu(s["w"][0]), k_weight=cu(s["w"][1]))
+    want = B.diffattn_qk_norm_rope_bwd(*args, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = B.diffattn_qk_norm_rope_bwd(*args, **kw)
+    for t in got.values():
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    # in place, as the attention's gradients are of no further use
+    q = dy[0].clone()
+    lib = B.load()
+    ws = torch.empty(B.diffattn_qk_norm_rope_bwd_workspace_size(300, 6, 2, 128),
+                     dtype=torch.uint8, device="cuda")
+    k = dy[1].clone()
+    st = lib.diffattn_qk_norm_rope_bwd(
+        s["qd"].data_ptr(), s["qd"].stride(0), s["kd"].data_ptr(), s["kd"].stride(0), B.DA_BF16,
+        q.data_ptr(), 6 * 128, k.data_ptr(), 2 * 128, 300, 6, 2, 128,
+        kw["q_weight"].data_ptr(), kw["k_weight"].data_ptr(), 1e-6, args[4].data_ptr(),
+        args[5].data_ptr(), 128, 0, q.data_ptr(), k.data_ptr(), None, None, ws.data_ptr(),
+        ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert st == B.DA_OK and torch.equal(q, want["dq"]) and torch.equal(k, want["dk"])
 
 
 def test_norm_gradient_continues_the_attention_backward(B):

@@ -167,6 +167,13 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ uint4 ldg128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -363,6 +370,28 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     span_of(a, b, lo, len);
     const int s0 = lo / kStageTokens + s_first;  // absolute stage
 
+    // The segment's queries: column g of column tile n, channels 32 * qd ...  They
+    // are asked for before the copies, which would hold them up for 3 us when
+    // all warps start at once.
+    uint32_t qf[NT][16];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = chunk * kChunkHeads + n * 8 + (int)g;
+      bool live = col < a.group;
+      const __nv_bfloat16* src;
+      if (kV1) {  // column 0 has features 0..63 of the head, column 1 the rest
+        src = a.q + ((size_t)b * a.heads + kvh) * kD + 32 * qd;
+        live = live && (g == qd / 2);
+      } else {
+        src = a.q + ((size_t)b * a.heads * a.group + (size_t)kvh * a.group + col) * kD + 32 * qd;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (live) u = ldg128(src + 8 * i);
+        qf[n][4 * i] = u.x, qf[n][4 * i + 1] = u.y, qf[n][4 * i + 2] = u.z, qf[n][4 * i + 3] = u.w;
+      }
+    }
     // The next 32 tiles (8 stages) of the segment, one per lane, and the 32
     // behind them.
     const int* row = a.table + (size_t)b * a.max_pages;
@@ -413,27 +442,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       if (++to == kRing) to = 0;
     }
 
-    // Query fragments: column g of tile n, channels 32 * qd ...
-    uint32_t qf[NT][16];
+    // Query fragments, from what was asked for above.
     float back[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int col = chunk * kChunkHeads + n * 8 + (int)g;
-      bool live = col < a.group;
-      const __nv_bfloat16* src;
-      if (kV1) {  // column 0 has features 0..63 of the head, column 1 the rest
-        src = a.q + ((size_t)b * a.heads + kvh) * kD + 32 * qd;
-        live = live && (g == qd / 2);
-      } else {
-        src = a.q + ((size_t)b * a.heads * a.group + (size_t)kvh * a.group + col) * kD + 32 * qd;
-      }
-      uint32_t raw[16];
+      uint32_t(&raw)[16] = qf[n];
       uint32_t top = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 u = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
-        raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
-      }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         top = max(top, max((raw[i] << 16) & 0x7F800000u, raw[i] & 0x7F800000u));
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
       const float down = __uint_as_float((254u - e) << 23);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        qf[n][i] = pack_f16(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
+        raw[i] = pack_f16(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
       // Positive, so that it can multiply a masked score's infinity; scores
       // that this floor touches are 0 to any precision here.
       const float up = fmaxf(__uint_as_float(e << 23) * a.scale, 1.0e-30f);

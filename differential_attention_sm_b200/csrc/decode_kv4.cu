@@ -38,6 +38,7 @@
 #include "diffattn.h"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace da {
@@ -169,7 +170,7 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32
 }
 __device__ __forceinline__ uint4 ldg128(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -310,7 +311,6 @@ template <int NT, bool kV1>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     kv4_decode_kernel(const Kv4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t lane = threadIdx.x & 31u;
   const int warp = (int)(threadIdx.x >> 5);
   const uint32_t g = lane >> 2, qd = lane & 3u;
@@ -325,6 +325,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     fence_proxy_async_smem();
   }
   __syncwarp();
+  after_previous();
+  let_next_start();  // not sooner: the second kernel reads the lengths before its own wait
 
   const int units = a.heads * a.chunks;  // of one sequence
   long long before, total;
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
     w0 = (int)divide(start, run);
     n = n_b > 0 ? (int)divide(start + n_b - 1, run) - w0 + 1 : 0;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   if (a.spans && n_b > 0) {
     const int2 v = a.spans[(size_t)b * units + unit];
     w0 = v.x, n = v.y;
@@ -761,24 +763,15 @@ cudaError_t launch(Kv4Args& a, void* workspace, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kWarps * 32, kSmemBytes, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3(grid), kWarps * 32, kSmemBytes, stream, a);
   };
   cudaError_t e;
   if (a.v1) e = run(kv4_decode_kernel<1, true>);
   else if (a.cols <= 8) e = run(kv4_decode_kernel<1, false>);
   else e = run(kv4_decode_kernel<2, false>);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)a.batch * (unsigned)a.out_heads);
-  cfg.blockDim = dim3(kCombineWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_combine_kernel, (const Kv4Args)a);
+  return launch_after(kv4_combine_kernel, dim3((unsigned)a.batch * (unsigned)a.out_heads),
+                      kCombineWarps * 32, 0, stream, a);
 }
 
 int check(const void* q, const void* cache, const int* table, const int* lens, const void* out,

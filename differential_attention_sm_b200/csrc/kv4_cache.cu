@@ -9,6 +9,7 @@
 #include "diffattn.h"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace da {
@@ -38,7 +39,7 @@ template <typename T>
 __device__ __forceinline__ Block<T> load_block(const T* p) {
   Block<T> b;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T); ++i) b.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  for (int i = 0; i < (int)sizeof(T); ++i) b.v[i] = reinterpret_cast<const uint4*>(p)[i];
   return b;
 }
 __device__ __forceinline__ void unpack(const Block<float>& b, float (&x)[16]) {
@@ -169,6 +170,8 @@ struct Lane {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const CacheArgs a) {
+  let_next_start();
+  after_previous();
   Lane w;
   if (w.tok >= a.tokens) return;
   const T* src = (w.is_v ? static_cast<const T*>(a.v) + w.tok * a.v_tok
@@ -233,6 +236,8 @@ __device__ __forceinline__ void store_block(__nv_bfloat16* p, const uint32_t (&h
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
   constexpr int kAtOnce = 4;  // heads asked for together
+  let_next_start();
+  after_previous();
   Lane w;
   if (w.tok >= a.tokens || !w.find(a, a.slots[w.tok])) return;
   T* dst = static_cast<T*>(w.is_v ? a.v_out : a.k_out) + (int64_t)w.tok * a.heads * kKv4Row +
@@ -247,8 +252,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const CacheArgs a) {
       c[k] = make_uint2(0u, 0u), s[k] = 0u;
       if (h < a.heads) {
         const uint8_t* tile = w.tile + h * w.head_bytes;
-        c[k] = __ldg(reinterpret_cast<const uint2*>(tile + w.codes));
-        s[k] = __ldg(tile + w.scale);
+        c[k] = *reinterpret_cast<const uint2*>(tile + w.codes);
+        s[k] = tile[w.scale];
       }
     }
 #pragma unroll
@@ -330,11 +335,10 @@ extern "C" int diffattn_kv4_append(const void* k, long long k_token_stride, cons
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const dim3 grid = da::grid_for(tokens, n_kv_heads);
-  if (dtype == DA_BF16)
-    da::kv4_append_kernel<__nv_bfloat16><<<grid, da::kThreads, 0, cs>>>(a);
-  else
-    da::kv4_append_kernel<float><<<grid, da::kThreads, 0, cs>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  const auto kernel = dtype == DA_BF16 ? da::kv4_append_kernel<__nv_bfloat16>
+                                       : da::kv4_append_kernel<float>;
+  return da::launch_after(kernel, grid, da::kThreads, 0, cs, a) == cudaSuccess ? DA_OK
+                                                                               : DA_ERR_CUDA;
 }
 
 extern "C" int diffattn_kv4_read(const void* cache, int n_pages, int page_size, const int* slots,
@@ -358,12 +362,11 @@ extern "C" int diffattn_kv4_read(const void* cache, int n_pages, int page_size, 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const dim3 grid = da::grid_for(tokens, n_kv_heads);
   const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
-  if (dtype == DA_BF16) {
-    if (wide) da::kv4_read_kernel<__nv_bfloat16, true><<<grid, da::kThreads, 0, cs>>>(a);
-    else da::kv4_read_kernel<__nv_bfloat16, false><<<grid, da::kThreads, 0, cs>>>(a);
-  } else {
-    if (wide) da::kv4_read_kernel<float, true><<<grid, da::kThreads, 0, cs>>>(a);
-    else da::kv4_read_kernel<float, false><<<grid, da::kThreads, 0, cs>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  const auto kernel = dtype == DA_BF16
+                          ? (wide ? da::kv4_read_kernel<__nv_bfloat16, true>
+                                  : da::kv4_read_kernel<__nv_bfloat16, false>)
+                          : (wide ? da::kv4_read_kernel<float, true>
+                                  : da::kv4_read_kernel<float, false>);
+  return da::launch_after(kernel, grid, da::kThreads, 0, cs, a) == cudaSuccess ? DA_OK
+                                                                               : DA_ERR_CUDA;
 }

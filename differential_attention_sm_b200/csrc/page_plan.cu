@@ -22,6 +22,7 @@
 #include "diffattn.h"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace da {
@@ -84,8 +85,9 @@ __device__ __forceinline__ int slot_of(const PlanArgs& a, int page, int pos, boo
 
 // `with_slots`: this launch writes the slot rows and table entries too.
 __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, int with_slots) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ long long sh[33];
+  let_next_start();
+  after_previous();
   const int tid = threadIdx.x, lane = tid & 31;
   const int ps = 1 << a.page_shift;
   int free0 = *a.count;
@@ -219,7 +221,8 @@ __device__ __forceinline__ int upper_request(F offset, int lo, int hi, int i) {
 __global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs a) {
   __shared__ int ends[2];
   __shared__ Request keep[kFillKeep];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  after_previous();
   const int first = blockIdx.x * kFillRows;
   const int last = min(first + kFillRows, a.n_slots) - 1;
   auto global = [&](int r) { return a.offsets[r]; };
@@ -274,6 +277,8 @@ struct ReleaseArgs {
 
 __global__ void __launch_bounds__(1024) page_release_kernel(const ReleaseArgs a) {
   __shared__ long long sh[33];
+  let_next_start();
+  after_previous();
   const int tid = threadIdx.x, lane = tid & 31;
   const int ps = 1 << a.page_shift;
   int free0 = *a.count;
@@ -394,19 +399,12 @@ extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, in
   a.depth = static_cast<int*>(workspace);
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  da::page_plan_kernel<<<1, da::threads_for(requests), 0, cs>>>(a, need == 0);
-  if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
+  if (da::launch_after(da::page_plan_kernel, dim3(1), da::threads_for(requests), 0, cs, a,
+                       (int)(need == 0)) != cudaSuccess)
+    return DA_ERR_CUDA;
   if (need > 0) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows));
-    cfg.blockDim = dim3(da::kFillThreads);
-    cfg.stream = cs;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, da::page_slots_kernel, (const da::PlanArgs)a) != cudaSuccess)
+    const dim3 grid((unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows));
+    if (da::launch_after(da::page_slots_kernel, grid, da::kFillThreads, 0, cs, a) != cudaSuccess)
       return DA_ERR_CUDA;
   }
   return DA_OK;
@@ -431,7 +429,8 @@ extern "C" int diffattn_page_release(const int* release, int* cache_lens, int* b
   a.page_shift = da::kv4_shift(page_size);
   a.n_pages = n_pages;
   a.dev_status = dev_status;
-  da::page_release_kernel<<<1, da::threads_for(requests), 0,
-                            static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return da::launch_after(da::page_release_kernel, dim3(1), da::threads_for(requests), 0,
+                          static_cast<cudaStream_t>(stream), a) == cudaSuccess
+             ? DA_OK
+             : DA_ERR_CUDA;
 }

@@ -221,6 +221,21 @@ __device__ __forceinline__ int clc_response(const void* resp) {
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel launched by launch_after
+// (launch.cuh) may start while the one before it in the stream still runs.
+// ---------------------------------------------------------------------------
+// Everything before this kernel in the stream is done and visible.  Comes
+// before a kernel's first access to global memory.  (No ld.global.nc in such a
+// kernel of what the one before may write: it changes while this one lives.)
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The next kernel's CTAs may be placed once all CTAs of this one have come here.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), no multicast
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const void* desc) {

@@ -27,6 +27,7 @@
 
 #include "diffattn.h"
 #include "kernels.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace da {
@@ -229,6 +230,8 @@ template <typename T, int G, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(const NormArgs a) {
   __shared__ __align__(16) float cs[2][kAngles];
   __shared__ __align__(16) float sn[2][kAngles];
+  let_next_start();
+  after_previous();
   const int j = threadIdx.x % G, g = threadIdx.x / G;
   const int per_tok = (kThreads / G) >> a.tok_log2;  // groups of a token
   const int t = g / per_tok;
@@ -350,7 +353,8 @@ template <typename T, int G, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   BwdSmem<T>& sh = *reinterpret_cast<BwdSmem<T>*>(smem);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
+  after_previous();
   const int j = threadIdx.x % G, g = threadIdx.x / G;
   const int per_tok = (kThreads / G) >> a.tok_log2;
   const int t = g / per_tok;
@@ -505,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(
 __global__ void __launch_bounds__(1024) qk_norm_dweight_kernel(const float* partial, int rows,
                                                                int d, float* dwq, float* dwk) {
   __shared__ double sh[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_start();
+  after_previous();
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   double v = 0.0;
@@ -643,11 +648,13 @@ extern "C" int diffattn_qk_norm_rope(const void* q, long long q_token_stride, co
   while (grid.y < (unsigned)turns && (long long)grid.x * grid.y < 148 * da::kCtasPerSm / 2) ++grid.y;
   if (grid.y > 65535u) grid.y = 65535u;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   da::dispatch(dtype, lanes, interleaved != 0, [&](auto t, auto g, auto il) {
-    da::qk_norm_rope_kernel<decltype(t), decltype(g)::value, decltype(il)::value>
-        <<<grid, da::kThreads, 0, cs>>>(a);
+    e = da::launch_after(
+        da::qk_norm_rope_kernel<decltype(t), decltype(g)::value, decltype(il)::value>, grid,
+        da::kThreads, 0, cs, a);
   });
-  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 extern "C" size_t diffattn_qk_norm_rope_bwd_workspace_size(int tokens, int n_q_heads,
@@ -710,27 +717,17 @@ extern "C" int diffattn_qk_norm_rope_bwd(
   a.tok_log2 = da::batch_log2(tokens, heads, lanes, rot_dim, 4);
   const int batches = (int)(((long long)tokens + (1 << a.tok_log2) - 1) >> a.tok_log2);
   const int ctas = batches < da::kBwdCtas ? batches : da::kBwdCtas;
+  cudaError_t e = cudaSuccess;
   da::dispatch(dtype, lanes, interleaved != 0, [&](auto t, auto g, auto il) {
     auto kernel = da::qk_norm_rope_bwd_kernel<decltype(t), decltype(g)::value, decltype(il)::value>;
     constexpr int kBytes = (int)sizeof(da::BwdSmem<decltype(t)>);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) ==
-        cudaSuccess)
-      kernel<<<ctas, da::kThreads, kBytes, cs>>>(a);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e == cudaSuccess) e = da::launch_after(kernel, dim3(ctas), da::kThreads, kBytes, cs, a);
   });
-  if (cudaGetLastError() != cudaSuccess) return DA_ERR_CUDA;
-  if (dq_weight || dk_weight) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((2 * head_dim + 31) / 32);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = cs;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, da::qk_norm_dweight_kernel, (const float*)a.partial, ctas,
-                           head_dim, dq_weight, dk_weight) != cudaSuccess)
-      return DA_ERR_CUDA;
-  }
+  if (e != cudaSuccess) return DA_ERR_CUDA;
+  if ((dq_weight || dk_weight) &&
+      da::launch_after(da::qk_norm_dweight_kernel, dim3((2 * head_dim + 31) / 32), 1024, 0, cs,
+                       a.partial, ctas, head_dim, dq_weight, dk_weight) != cudaSuccess)
+    return DA_ERR_CUDA;
   return DA_OK;
 }

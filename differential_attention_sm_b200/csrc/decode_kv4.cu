@@ -26,8 +26,16 @@
 //    rounded to fp16 (half a step is 2^-11 of a probability; the sums l and O
 //    are fp32).  m moves only when a score passes it by more than 2^10, so p
 //    reaches 2^15 at most and the common stage needs no maximum across lanes.
-// A run that ends or begins inside a sequence leaves (O, l, m) in the
+// A run leaves (O, l, m) of each sequence and head that it touches in the
 // workspace; a second kernel joins them, subtracts, and normalises.
+//
+// Measured, 64 sequences of 32768 entries, 8 KV heads, 64 query heads (2.4 GB):
+// 376 to 415 us in bursts at 1965 MHz, 0.98 to 0.89 of the copy rate, 430 to
+// 445 us when the board's power limit sets the clock; the copies alone take 365.
+// A tile and head costs 238 instructions: 64 conversions, 64 multiplications
+// and 16 matrix instructions, which hold the former two up for 7 of their 8
+// clocks, make 285 of about 400 clocks of an SM quarter, where the memory
+// allows 405 at 1965 MHz.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

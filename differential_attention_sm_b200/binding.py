@@ -799,7 +799,7 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
         workspace = _workspace(None, need, at, stream)
     _run((_lib or load()).diffattn_page_plan, at, stream, new_lens.data_ptr(), cache_lens.data_ptr(),
          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
-         n_pages, page_size, n_slots, slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
+         n_pages, int(page_size), int(n_slots), slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
          served.data_ptr(), lens.data_ptr(), count.data_ptr(), _ptr(workspace),
          0 if workspace is None else workspace.nbytes, _ptr(dev_status))
     return out
@@ -813,7 +813,7 @@ def diffattn_page_release(release, cache_lens, block_table, free_pages, free_cou
     at = _one_device(release, cache_lens, block_table, free_pages, free_count, dev_status)
     _run((_lib or load()).diffattn_page_release, at, stream, release.data_ptr(), cache_lens.data_ptr(),
          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
-         n_pages, page_size, _ptr(dev_status))
+         n_pages, int(page_size), _ptr(dev_status))
 
 
 def diffattn_kv4_page_bytes(n_kv_heads, head_dim, page_size) -> int:
@@ -885,7 +885,7 @@ def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
     ws = _workspace(workspace, 0 if workspace is not None else
                     diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv), at, stream)
     _run((_lib or load()).diffattn_v2_decode_kv4, at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
-         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), window, out.data_ptr(), code, B,
+         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), int(window), out.data_ptr(), code, B,
          Hq, Hkv, d, lam.data_ptr(), ws.data_ptr(), ws.nbytes, _ptr(dev_status))
     return out
 
@@ -932,9 +932,9 @@ def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
     ws = _workspace(workspace, 0 if workspace is not None else
                     diffattn_v1_decode_kv4_workspace_size(B, H), at, stream)
     _run((_lib or load()).diffattn_v1_decode_kv4, at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
-         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), window, out.data_ptr(), code, B,
-         H, d2 // 2, 128, lam.data_ptr(), int(bool(apply_norm)), _ptr(norm_weight), norm_eps,
-         lambda_init, ws.data_ptr(), ws.nbytes, _ptr(dev_status))
+         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), int(window), out.data_ptr(), code, B,
+         H, d2 // 2, 128, lam.data_ptr(), int(bool(apply_norm)), _ptr(norm_weight), float(norm_eps),
+         float(lambda_init), ws.data_ptr(), ws.nbytes, _ptr(dev_status))
     return out
 
 
@@ -996,7 +996,7 @@ def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=
             kos = _token_stride("k out", ko, T, q.dtype)
         at = _one_device(q, k, positions, inv_freq, q_weight, k_weight, qo, ko)
     _run((_lib or load()).diffattn_qk_norm_rope, at, stream, q.data_ptr(), qs, _ptr(k), ks, code, T, Hq, Hk, d,
-         _ptr(q_weight), _ptr(k_weight), norm_eps, _ptr(positions), _ptr(inv_freq), rot,
+         _ptr(q_weight), _ptr(k_weight), float(norm_eps), _ptr(positions), _ptr(inv_freq), rot,
          int(bool(interleaved)), qo.data_ptr(), qos, _ptr(ko), kos)
     return qo, ko
 
@@ -1034,7 +1034,7 @@ def diffattn_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, *, q_we
                     diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), at, stream)
     _run((_lib or load()).diffattn_qk_norm_rope_bwd, at, stream, q.data_ptr(), qs, _ptr(k), ks, code,
          dq_out.data_ptr(), gqs, _ptr(dk_out), gks, T, Hq, Hk, d, _ptr(q_weight), _ptr(k_weight),
-         norm_eps, _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
+         float(norm_eps), _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
          r["dq"].data_ptr(), _ptr(r["dk"]), _ptr(r["dq_weight"]), _ptr(r["dk_weight"]),
          ws.data_ptr(), ws.nbytes)
     return r

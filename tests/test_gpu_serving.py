@@ -254,6 +254,25 @@ def test_cache_skips_slots_out_of_range(B):
     assert not k[0].any() and not k[2].any()
 
 
+@pytest.mark.parametrize("dtype,off", [(torch.bfloat16, 8), (torch.float32, 4),
+                                       (torch.bfloat16, 16), (torch.float32, 8)])
+def test_read_into_rows_on_16_bytes(B, dtype, off):
+    """Outputs that start on an odd or an even multiple of 16 bytes."""
+    T, H = 21, 3
+    x = torch.randn(T, H, 128, device="cuda")
+    cache = torch.zeros(3, H, 16 * 144, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(T, dtype=I32, device="cuda")
+    B.diffattn_kv4_append(x, 2 * x, slots, cache)
+    want = B.diffattn_kv4_read(cache, slots, dtype=dtype)
+    n = T * H * 128
+    flat = torch.full((2, n + 64), 7.0, dtype=dtype, device="cuda")
+    got = tuple(r[off:off + n].view(T, H, 128) for r in flat)
+    assert got[0].data_ptr() % 16 == 0
+    B.diffattn_kv4_read(cache, slots, out=got)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (flat[:, :off] == 7).all() and (flat[:, off + n:] == 7).all()
+
+
 def test_cache_no_tokens(B):
     cache = torch.zeros(2, 1, 16 * 144, dtype=torch.uint8, device="cuda")
     x = torch.ones(0, 1, 128, device="cuda")

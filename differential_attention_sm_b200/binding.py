@@ -651,114 +651,25 @@ def diffattn_selftest_wait_timeout(timeout_us, dev_status, waited_ns=None, strea
 
 
 # ---- serving: page plan, 4-bit paged cache, decode over it; QK norm + rotation
-# These calls take microseconds on the GPU, as long as a few checks take here.
-# So each call first asks in one expression whether all is as it should be, and
-# only otherwise goes through the named checks, which say what is not; devices
-# are compared by index, and switched only when the device is not the current.
-_I32, _U8, _F32, _BF16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
-_CODES = {_BF16: DA_BF16, _F32: DA_FP32}
+# These calls take 3 to 10 us on the GPU, less than their checks and arguments
+# take in Python, so a compiled module (csrc/marshal.cpp) does those.  It makes
+# the tensors' device current and takes that device's current stream unless
+# `stream` is given.  Wrong types raise TypeError, wrong shapes ValueError.
+_marshal = None
 
 
-def _need(name, t, dtype, shape=None):
-    """A dense tensor of one type and shape (None: any)."""
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-
-
-def _one_device(first, *others):
-    """Index of the device that all tensors of a call lie on."""
-    at = first.get_device()
-    if at < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != at:
-            raise ValueError("tensors lie on different devices (cuda:%d, %s)" % (at, t.device))
-    return at
-
-
-def _run(fn, at, stream, *args):
-    """Calls an entry point with device `at` current, on `stream` (None: that
-    device's current stream)."""
-    if torch._C._cuda_getDevice() != at:
-        with torch.cuda.device(at):
-            status = fn(*args, _stream(stream))
-    else:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None
-                    else _stream(stream))
-    if status != DA_OK:
-        raise DiffAttnError(fn.__name__, status)
-
-
-def _token_stride(name, t, tokens=None, dtype=None):
-    """Token stride of t [T, H, d], whose heads of a token lie in a row."""
-    if t.dim() != 3 or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError("%s must be [tokens, heads, width], got %s" % (name, tuple(t.shape)))
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    T, H, d = t.shape
-    st, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (H > 1 and sh != d):
-        raise ValueError("%s: the heads of a token must lie in a row" % name)
-    return st if T > 1 else max(1, H) * d
-
-
-def _code(name, t):
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError("%s: unsupported dtype %s" % (name, t.dtype))
-    return code
-
-
-def _workspace(workspace, need, at, stream):
-    if workspace is None:
-        device = torch.device("cuda", at)
-        workspace = torch.empty(max(need, 1), dtype=_U8, device=device)
-        if stream is not None:   # freed on return: kept from reuse until that stream is past it
-            workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=device))
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace
-
-
-def _kv4_cache(cache):
-    """(pages, KV heads, page size) of a cache [n_pages, n_kv_heads, page_size * 144]."""
-    if cache.dtype is not _U8 or not cache.is_contiguous():
-        _need("cache", cache, _U8)
-    if cache.dim() == 3:
-        pages, heads, nbytes = cache.shape
-        if nbytes % 144 == 0:
-            return pages, heads, nbytes // 144
-    raise ValueError("cache must be [n_pages, n_kv_heads, page_size * 144], not %s"
-                     % (tuple(cache.shape),))
-
-
-def _page_lists(first, cache_lens, block_table, free_pages, free_count):
-    """(requests, max_pages, n_pages), all checked."""
-    R = first.numel()
-    if (first.dtype is _I32 and cache_lens.dtype is _I32 and block_table.dtype is _I32 and
-            free_pages.dtype is _I32 and free_count.dtype is _I32 and first.is_contiguous() and
-            cache_lens.is_contiguous() and block_table.is_contiguous() and
-            free_pages.is_contiguous() and free_count.numel() == 1 and
-            first.dim() == cache_lens.dim() == free_pages.dim() == free_count.dim() == 1 and
-            cache_lens.numel() == R and block_table.dim() == 2):
-        rows, max_pages = block_table.shape
-        if rows == R:
-            return R, max_pages, free_pages.numel()
-    _need("new_lens or release", first, _I32, (R,))
-    _need("cache_lens", cache_lens, _I32, (R,))
-    _need("block_table", block_table, _I32)
-    _need("free_pages", free_pages, _I32)
-    _need("free_count", free_count, _I32, (1,))
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table must be [%d, max_pages], not %s"
-                         % (R, tuple(block_table.shape)))
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [n_pages]")
-    return R, block_table.shape[1], free_pages.shape[0]
+def _serving():
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise ImportError("_marshal.so not built (run __graft_entry__.build() or "
+                              "python -m differential_attention_sm_b200.build)") from e
+        m.bind(lib._handle, DiffAttnError)
+        _marshal = m
+    return _marshal
 
 
 def diffattn_page_plan_workspace_size(requests, n_slots) -> int:
@@ -774,46 +685,17 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
     [R + 1], served, cache_lens [R], free_count [1] (int32).  `out`, such a
     dict, is written instead of new tensors; its cache_lens and free_count
     may be the arguments themselves."""
-    R, max_pages, n_pages = _page_lists(new_lens, cache_lens, block_table, free_pages, free_count)
-    if n_slots < 0:
-        raise ValueError("n_slots is negative")
-    need = 0
-    if workspace is None and n_slots > 1024:   # none below
-        need = diffattn_page_plan_workspace_size(R, n_slots)
-    if out is None:
-        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, workspace,
-                         dev_status)
-        slots, positions, offsets, served, lens, count = new_lens.new_empty(
-            2 * n_slots + 3 * R + 2).split_with_sizes((n_slots, n_slots, R + 1, R, R, 1))
-        out = {"slots": slots, "positions": positions, "offsets": offsets, "served": served,
-               "cache_lens": lens, "free_count": count}
-    else:
-        for name, n in (("slots", n_slots), ("positions", n_slots), ("offsets", R + 1),
-                        ("served", R), ("cache_lens", R), ("free_count", 1)):
-            _need(name, out[name], _I32, (n,))
-        slots, positions, offsets, served, lens, count = (out[name] for name in (
-            "slots", "positions", "offsets", "served", "cache_lens", "free_count"))
-        at = _one_device(new_lens, cache_lens, block_table, free_pages, free_count, workspace,
-                         dev_status, slots, positions, offsets, served, lens, count)
-    if need:
-        workspace = _workspace(None, need, at, stream)
-    _run((_lib or load()).diffattn_page_plan, at, stream, new_lens.data_ptr(), cache_lens.data_ptr(),
-         block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
-         n_pages, int(page_size), int(n_slots), slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
-         served.data_ptr(), lens.data_ptr(), count.data_ptr(), _ptr(workspace),
-         0 if workspace is None else workspace.nbytes, _ptr(dev_status))
-    return out
+    return (_marshal or _serving()).page_plan(
+        new_lens, cache_lens, block_table, free_pages, free_count, page_size, n_slots, out,
+        workspace, dev_status, stream)
 
 
 def diffattn_page_release(release, cache_lens, block_table, free_pages, free_count, page_size, *,
                           dev_status=None, stream=None):
     """Gives the pages of requests with release[r] != 0 back (int32 [R]);
     cache_lens, block_table, free_pages and free_count are changed in place."""
-    R, max_pages, n_pages = _page_lists(release, cache_lens, block_table, free_pages, free_count)
-    at = _one_device(release, cache_lens, block_table, free_pages, free_count, dev_status)
-    _run((_lib or load()).diffattn_page_release, at, stream, release.data_ptr(), cache_lens.data_ptr(),
-         block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), R, max_pages,
-         n_pages, int(page_size), _ptr(dev_status))
+    (_marshal or _serving()).page_release(release, cache_lens, block_table, free_pages, free_count,
+                                          page_size, dev_status, stream)
 
 
 def diffattn_kv4_page_bytes(n_kv_heads, head_dim, page_size) -> int:
@@ -824,43 +706,21 @@ def diffattn_kv4_append(k, v, slots, cache, *, dev_status=None, stream=None):
     """Writes rows k, v [T, Hkv, 128] (bf16 or fp32; slices of a fused
     projection are taken as they are) into the 4-bit cache
     [n_pages, Hkv, page_size * 144] uint8 at slots int32 [T] (negative: skipped)."""
-    if v.shape != k.shape:
-        raise ValueError("k and v differ in shape")
-    dtype = _code("k", k)
-    ks, vs = _token_stride("k", k), _token_stride("v", v, None, k.dtype)
-    T, H, d = k.shape
-    if slots.dtype is not _I32 or slots.shape != (T,) or not slots.is_contiguous():
-        _need("slots", slots, _I32, (T,))
-    pages, heads, ps = _kv4_cache(cache)
-    if heads != H:
-        raise ValueError("cache holds %d heads, k %d" % (heads, H))
-    at = _one_device(k, v, slots, cache, dev_status)
-    _run((_lib or load()).diffattn_kv4_append, at, stream, k.data_ptr(), ks, v.data_ptr(), vs, dtype,
-         slots.data_ptr(), T, H, d, cache.data_ptr(), pages, ps, _ptr(dev_status))
-    return cache
+    return (_marshal or _serving()).kv4_append(k, v, slots, cache, dev_status, stream)
 
 
 def diffattn_kv4_read(cache, slots, *, out=None, dtype=torch.bfloat16, dev_status=None,
                       stream=None):
     """Rows (k, v) [T, Hkv, 128] held at slots int32 [T].  Rows of negative
     slots are left as they were in `out` = (k, v), or are 0 in new tensors."""
-    pages, H, ps = _kv4_cache(cache)
-    if slots.dtype is not _I32 or slots.dim() != 1 or not slots.is_contiguous():
-        _need("slots", slots, _I32, (slots.numel(),))
-    T = slots.shape[0]
     if out is None:
-        out = tuple(torch.zeros(T, H, 128, dtype=dtype, device=cache.device) for _ in "kv")
-    k, v = out
-    code = _code("k", k)
-    shape = (T, H, 128)
-    if (v.dtype is not k.dtype or k.shape != shape or v.shape != shape or
-            not k.is_contiguous() or not v.is_contiguous()):
-        _need("k", k, k.dtype, shape)
-        _need("v", v, k.dtype, shape)
-    at = _one_device(cache, slots, k, v, dev_status)
-    _run((_lib or load()).diffattn_kv4_read, at, stream, cache.data_ptr(), pages, ps, slots.data_ptr(), T, H, 128,
-         k.data_ptr(), v.data_ptr(), code, _ptr(dev_status))
-    return k, v
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("unsupported dtype %s" % dtype)
+        k = v = None
+    else:
+        k, v = out
+    return (_marshal or _serving()).kv4_read(
+        cache, slots, k, v, DA_BF16 if dtype is torch.bfloat16 else DA_FP32, dev_status, stream)
 
 
 def diffattn_v2_decode_kv4_workspace_size(batch, n_q_heads, n_kv_heads) -> int:
@@ -872,37 +732,9 @@ def diffattn_v2_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
     """V2 decode over the 4-bit cache.  q [B, Hq, 128] bf16; cache
     [n_pages, Hkv, page_size * 144] uint8; block_table int32 [B, max_pages];
     cache_lens int32 [B]; lam [Hq/2] fp32; out [B, Hq/2, 128]."""
-    code = _code("q", q)
-    B, Hq, d = q.shape
-    _need("q", q, q.dtype)
-    pages, Hkv, ps = _kv4_cache(cache)
-    max_pages = _decode_lists(B, block_table, cache_lens, lam, Hq // 2)
-    at = _one_device(q, cache, block_table, cache_lens, lam, workspace, out, dev_status)
-    if out is None:
-        out = q.new_empty((B, Hq // 2, d))
-    else:
-        _need("out", out, q.dtype, (B, Hq // 2, d))
-    ws = _workspace(workspace, 0 if workspace is not None else
-                    diffattn_v2_decode_kv4_workspace_size(B, Hq, Hkv), at, stream)
-    _run((_lib or load()).diffattn_v2_decode_kv4, at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
-         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), int(window), out.data_ptr(), code, B,
-         Hq, Hkv, d, lam.data_ptr(), ws.data_ptr(), ws.nbytes, _ptr(dev_status))
-    return out
-
-
-def _decode_lists(B, block_table, cache_lens, lam, n_lam):
-    """max_pages of a decode's tables, all checked."""
-    if (block_table.dtype is not _I32 or cache_lens.dtype is not _I32 or lam.dtype is not _F32 or
-            cache_lens.shape != (B,) or lam.shape != (n_lam,) or
-            not block_table.is_contiguous() or not cache_lens.is_contiguous() or
-            not lam.is_contiguous()):
-        _need("block_table", block_table, _I32)
-        _need("cache_lens", cache_lens, _I32, (B,))
-        _need("lam", lam, _F32, (n_lam,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [%d, max_pages], not %s"
-                         % (B, tuple(block_table.shape)))
-    return block_table.shape[1]
+    return (_marshal or _serving()).decode_kv4(
+        2, q, cache, block_table, cache_lens, lam, window, False, None, 0.0, 0.0, workspace, out,
+        dev_status, stream)
 
 
 def diffattn_v1_decode_kv4_workspace_size(batch, n_heads) -> int:
@@ -914,61 +746,9 @@ def diffattn_v1_decode_kv4(q, cache, block_table, cache_lens, lam, *, window=0, 
                            out=None, dev_status=None, stream=None):
     """V1 decode over the 4-bit cache.  q [B, H, 128] bf16 (two 64-wide
     branches); cache [n_pages, H, page_size * 144] uint8; out [B, H, 128]."""
-    code = _code("q", q)
-    B, H, d2 = q.shape
-    _need("q", q, q.dtype)
-    pages, heads, ps = _kv4_cache(cache)
-    if heads != H:
-        raise ValueError("cache holds %d heads, q %d" % (heads, H))
-    max_pages = _decode_lists(B, block_table, cache_lens, lam, H)
-    if norm_weight is not None:
-        _need("norm_weight", norm_weight, _F32, (128,))
-    at = _one_device(q, cache, block_table, cache_lens, lam, norm_weight, workspace, out,
-                     dev_status)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need("out", out, q.dtype, (B, H, 128))
-    ws = _workspace(workspace, 0 if workspace is not None else
-                    diffattn_v1_decode_kv4_workspace_size(B, H), at, stream)
-    _run((_lib or load()).diffattn_v1_decode_kv4, at, stream, q.data_ptr(), cache.data_ptr(), pages, ps,
-         block_table.data_ptr(), max_pages, cache_lens.data_ptr(), int(window), out.data_ptr(), code, B,
-         H, d2 // 2, 128, lam.data_ptr(), int(bool(apply_norm)), _ptr(norm_weight), float(norm_eps),
-         float(lambda_init), ws.data_ptr(), ws.nbytes, _ptr(dev_status))
-    return out
-
-
-def _norm_rope_args(q, k, positions, inv_freq, q_weight, k_weight):
-    dtype = q.dtype
-    code = _code("q", q)
-    T, Hq, d = q.shape
-    qs, sh, sd = q.stride()
-    if sd != 1 or sh != d or T < 2:
-        qs = _token_stride("q", q)
-    Hk = ks = 0
-    if k is not None:
-        Tk, Hk, dk = k.shape
-        ks, sh, sd = k.stride()
-        if sd != 1 or sh != d or Tk != T or T < 2 or k.dtype is not dtype:
-            ks = _token_stride("k", k, T, dtype)
-        if dk != d:
-            raise ValueError("q and k differ in width")
-    if q_weight is not None and (q_weight.dtype is not _F32 or q_weight.shape != (d,) or
-                                 not q_weight.is_contiguous()):
-        _need("q_weight", q_weight, _F32, (d,))
-    if k_weight is not None and (k_weight.dtype is not _F32 or k_weight.shape != (d,) or
-                                 not k_weight.is_contiguous()):
-        _need("k_weight", k_weight, _F32, (d,))
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        if (inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or
-                not inv_freq.is_contiguous()):
-            _need("inv_freq", inv_freq, _F32, (rot // 2,))
-    if positions is not None and (positions.dtype is not _I32 or positions.shape != (T,) or
-                                  not positions.is_contiguous()):
-        _need("positions", positions, _I32, (T,))
-    return code, T, Hq, Hk, d, qs, ks, rot
+    return (_marshal or _serving()).decode_kv4(
+        1, q, cache, block_table, cache_lens, lam, window, apply_norm, norm_weight, norm_eps,
+        lambda_init, workspace, out, dev_status, stream)
 
 
 def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
@@ -978,27 +758,9 @@ def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=
     (None: ones), then the rotation of the first 2 * len(inv_freq) features by
     positions int32 [T] * inv_freq fp32 (inv_freq None: no rotation).  k may
     be None.  Returns (q, k); `out` = (q, k) may be the arguments themselves."""
-    code, T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight,
-                                                      k_weight)
-    ko, kos = None, 0
-    if out is None:
-        # dense, since a token's heads lie in a row and tokens do not overlap
-        qo, qos = torch.empty_like(q), Hq * d
-        if k is not None:
-            ko, kos = torch.empty_like(k), Hk * d
-        at = _one_device(q, k, positions, inv_freq, q_weight, k_weight)
-    else:
-        qo, ko = out
-        if qo.shape != q.shape or (k is not None and ko.shape != k.shape):
-            raise ValueError("outputs must have the inputs' shapes")
-        qos = _token_stride("q out", qo, T, q.dtype)
-        if k is not None:
-            kos = _token_stride("k out", ko, T, q.dtype)
-        at = _one_device(q, k, positions, inv_freq, q_weight, k_weight, qo, ko)
-    _run((_lib or load()).diffattn_qk_norm_rope, at, stream, q.data_ptr(), qs, _ptr(k), ks, code, T, Hq, Hk, d,
-         _ptr(q_weight), _ptr(k_weight), float(norm_eps), _ptr(positions), _ptr(inv_freq), rot,
-         int(bool(interleaved)), qo.data_ptr(), qos, _ptr(ko), kos)
-    return qo, ko
+    qo, ko = out or (None, None)
+    return (_marshal or _serving()).qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight,
+                                                 norm_eps, interleaved, qo, ko, stream)
 
 
 def diffattn_qk_norm_rope_bwd_workspace_size(tokens, n_q_heads, n_k_heads, head_dim) -> int:
@@ -1012,32 +774,9 @@ def diffattn_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, *, q_we
     """Gradients of diffattn_qk_norm_rope: q, k are its inputs, dq_out, dk_out
     (fp32) the gradients of its outputs.  Returns a dict of fp32 tensors: dq,
     dk, dq_weight, dk_weight (None where the input is None)."""
-    code, T, Hq, Hk, d, qs, ks, rot = _norm_rope_args(q, k, positions, inv_freq, q_weight,
-                                                      k_weight)
-    if dq_out.shape != q.shape or (k is not None and dk_out.shape != k.shape):
-        raise ValueError("the gradients must have the inputs' shapes")
-    if dq_out.dtype is _F32 and dq_out.is_contiguous():
-        gqs = Hq * d
-    else:
-        gqs = _token_stride("dq_out", dq_out, T, _F32)
-    if k is None:
-        gks = 0
-    elif dk_out.dtype is _F32 and dk_out.is_contiguous():
-        gks = Hk * d
-    else:
-        gks = _token_stride("dk_out", dk_out, T, _F32)
-    at = _one_device(q, k, dq_out, dk_out, positions, inv_freq, q_weight, k_weight, workspace)
-    r = {"dq": torch.empty_like(dq_out), "dk": None if k is None else torch.empty_like(dk_out),
-         "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
-         "dk_weight": None if k is None or k_weight is None else torch.empty_like(k_weight)}
-    ws = _workspace(workspace, 0 if workspace is not None else
-                    diffattn_qk_norm_rope_bwd_workspace_size(T, Hq, Hk, d), at, stream)
-    _run((_lib or load()).diffattn_qk_norm_rope_bwd, at, stream, q.data_ptr(), qs, _ptr(k), ks, code,
-         dq_out.data_ptr(), gqs, _ptr(dk_out), gks, T, Hq, Hk, d, _ptr(q_weight), _ptr(k_weight),
-         float(norm_eps), _ptr(positions), _ptr(inv_freq), rot, int(bool(interleaved)),
-         r["dq"].data_ptr(), _ptr(r["dk"]), _ptr(r["dq_weight"]), _ptr(r["dk_weight"]),
-         ws.data_ptr(), ws.nbytes)
-    return r
+    return (_marshal or _serving()).qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq,
+                                                     q_weight, k_weight, norm_eps, interleaved,
+                                                     workspace, stream)
 
 
 def diffattn_reset_tile_counters(stream=None):

@@ -4,8 +4,8 @@
 // to the library's C entry points; all arithmetic happens there.
 //
 // These calls take 3 to 10 us on the GPU.  Checked and passed from Python they
-// took 13 to 20 us (the norm's 21 arguments 2, its checks 2, its two outputs 3),
-// from here 6 to 9.
+// took 13 to 20 us (the norm: 21 arguments 2, checks 2, two outputs 3),
+// from here 6 to 11 with their launches.
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
@@ -259,6 +259,16 @@ Lists page_lists(const char* first_name, const at::Tensor& first, const at::Tens
           as_int("the number of pages", pages.numel())};
 }
 
+// Elements [from, from + n) of a flat tensor that needs no gradient, without the
+// dispatcher's view bookkeeping (six views cost 4 us through it).
+at::Tensor piece(const at::Tensor& flat, int64_t from, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::TensorImpl::VIEW, c10::Storage(flat.storage()), flat.key_set(), flat.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(flat.storage_offset() + from);
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{n}, at::IntArrayRef{1});
+  return t;
+}
+
 constexpr const char* kPlanNames[6] = {"slots",  "positions",  "offsets",
                                        "served", "cache_lens", "free_count"};
 
@@ -293,22 +303,32 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   On on(a[10], new_lens, lens, table, pages, n_free, ws, status, out[0], out[1], out[2], out[3],
         out[4], out[5]);
+  // New outputs, and the scratch if none was brought, are pieces of one allocation.
+  void* scratch = ws ? ws->data_ptr() : nullptr;
+  size_t scratch_bytes = ws ? ws->nbytes() : 0;
+  if (ws && !ws->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+  at::Tensor own;
+  const size_t scratch_need = ws ? 0 : lib.diffattn_page_plan_workspace_size(s.requests, n_slots);
   if (fresh) {
-    const at::Tensor flat = at::empty({2 * (int64_t)n_slots + 3 * R + 2}, new_lens.options());
+    const int64_t pieces = 2 * (int64_t)n_slots + 3 * R + 2;
+    own = at::empty({pieces + (int64_t)(scratch_need + 3) / 4}, new_lens.options());
     int64_t from = 0;
     for (int i = 0; i < 6; ++i) {
-      out[i] = flat.narrow(0, from, sizes[i]);
+      out[i] = piece(own, from, sizes[i]);
       from += sizes[i];
     }
+    scratch = scratch_need ? address<int>(own) + pieces : scratch;
+  } else if (scratch_need) {
+    own = on.scratch(scratch_need);
+    scratch = own.data_ptr();
   }
-  Scratch scratch(on, ws,
-                  [&] { return lib.diffattn_page_plan_workspace_size(s.requests, n_slots); });
+  if (scratch_need) scratch_bytes = scratch_need;
   call("diffattn_page_plan", [&] {
     return lib.diffattn_page_plan(
         address<int>(new_lens), address<int>(lens), address<int>(table), address<int>(pages),
         address<int>(n_free), s.requests, s.max_pages, s.n_pages, page_size, n_slots,
         address<int>(out[0]), address<int>(out[1]), address<int>(out[2]), address<int>(out[3]),
-        address<int>(out[4]), address<int>(out[5]), scratch.p, scratch.bytes,
+        address<int>(out[4]), address<int>(out[5]), scratch, scratch_bytes,
         address<int>(status), on.stream());
   });
   if (!fresh) return Py_NewRef(a[7]);

@@ -61,6 +61,12 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 const at::Tensor* optional(PyObject* o, const char* name) {
   return o == Py_None ? nullptr : &tensor(o, name);
 }
+const at::Tensor* status_word(PyObject* o) {
+  const at::Tensor* t = optional(o, "dev_status");
+  if (t && (t->scalar_type() != at::kInt || t->numel() < 1))
+    refuse(PyExc_TypeError, "dev_status must be an int32 word");
+  return t;
+}
 int64_t integer(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw python_error();
@@ -132,7 +138,8 @@ int64_t token_stride(const char* name, const at::Tensor& t, int64_t tokens, at::
   return token_stride(name, t);
 }
 
-// A call's device, made current for it, and its stream.
+// A call's device and stream, made current for it: what it allocates (and fills)
+// is ordered on that stream.
 class On {
  public:
   template <typename... Ts>
@@ -141,7 +148,6 @@ class On {
     if (stream == Py_None) {
       stream_ = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index_).stream();
     } else {
-      own_ = true;
       if (PyLong_Check(stream)) {
         stream_ = (cudaStream_t)(uintptr_t)integer(stream);
       } else {
@@ -151,18 +157,16 @@ class On {
         Py_DECREF(raw);
         if (PyErr_Occurred()) throw python_error();
       }
+      stream_guard_.reset_stream(
+          c10::cuda::getStreamFromExternal(stream_, (c10::DeviceIndex)index_).unwrap());
     }
   }
   void* stream() const { return stream_; }
   // Scratch of a call that brings none.
   at::Tensor scratch(size_t bytes) const {
-    at::Tensor t = at::empty({(int64_t)(bytes ? bytes : 1)},
-                             at::TensorOptions()
-                                 .dtype(at::kByte)
-                                 .device(at::kCUDA, (c10::DeviceIndex)index_));
-    if (own_)  // freed on return: kept from reuse until that stream is past it
-      t.record_stream(c10::cuda::getStreamFromExternal(stream_, (c10::DeviceIndex)index_).unwrap());
-    return t;
+    return at::empty({(int64_t)(bytes ? bytes : 1)},
+                     at::TensorOptions().dtype(at::kByte).device(at::kCUDA,
+                                                                 (c10::DeviceIndex)index_));
   }
 
  private:
@@ -180,8 +184,8 @@ class On {
   }
   int index_;
   c10::cuda::CUDAGuard guard_;
+  c10::cuda::OptionalCUDAStreamGuard stream_guard_;
   cudaStream_t stream_ = nullptr;
-  bool own_ = false;
 };
 
 template <typename T = void>
@@ -283,7 +287,7 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Lists s = page_lists("new_lens", new_lens, lens, table, pages, n_free);
   const int page_size = small(a[5], "page_size"), n_slots = small(a[6], "n_slots");
   if (n_slots < 0) refuse(PyExc_ValueError, "n_slots is negative");
-  const at::Tensor *ws = optional(a[8], "workspace"), *status = optional(a[9], "dev_status");
+  const at::Tensor *ws = optional(a[8], "workspace"), *status = status_word(a[9]);
   const int64_t R = s.requests;
   const int64_t sizes[6] = {n_slots, n_slots, R + 1, R, R, 1};
   at::Tensor out[6];
@@ -348,7 +352,7 @@ PyObject* page_release(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    &n_free = tensor(a[4], "free_count");
   const Lists s = page_lists("release", release, lens, table, pages, n_free);
   const int page_size = small(a[5], "page_size");
-  const at::Tensor* status = optional(a[6], "dev_status");
+  const at::Tensor* status = status_word(a[6]);
   On on(a[7], release, lens, table, pages, n_free, status);
   call("diffattn_page_release", [&] {
     return lib.diffattn_page_release(address<int>(release), address<int>(lens),
@@ -386,7 +390,7 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Cache c = kv4_cache(cache);
   if (c.heads != k.size(1))
     refuse(PyExc_ValueError, "cache holds %d heads, k %lld", c.heads, (long long)k.size(1));
-  const at::Tensor* status = optional(a[4], "dev_status");
+  const at::Tensor* status = status_word(a[4]);
   On on(a[5], k, v, slots, cache, status);
   const int tokens = as_int("the number of tokens", k.size(0)),
             width = as_int("the width", k.size(2));
@@ -407,7 +411,7 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Cache c = kv4_cache(cache);
   need("slots", slots, at::kInt, {slots.numel()});
   const int64_t T = slots.numel();
-  const at::Tensor* status = optional(a[5], "dev_status");
+  const at::Tensor* status = status_word(a[5]);
   const bool fresh = a[2] == Py_None;
   at::Tensor k, v;
   if (!fresh) {
@@ -470,7 +474,7 @@ PyObject* decode_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need("lam", lam, at::kFloat, {heads});
   const int window = small(a[6], "window");
   const at::Tensor *gain = optional(a[8], "norm_weight"), *ws = optional(a[11], "workspace"),
-                   *given = optional(a[12], "out"), *status = optional(a[13], "dev_status");
+                   *given = optional(a[12], "out"), *status = status_word(a[13]);
   if (gain) need("norm_weight", *gain, at::kFloat, {128});
   const int64_t width = v1 ? 128 : d;
   if (given) need("out", *given, q.scalar_type(), {B, heads, width});

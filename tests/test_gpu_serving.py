@@ -273,6 +273,35 @@ def test_read_into_rows_on_16_bytes(B, dtype, off):
     assert (flat[:, :off] == 7).all() and (flat[:, off + n:] == 7).all()
 
 
+def test_other_streams_order_what_a_call_allocates(B):
+    """Calls on a stream of their own that bring no outputs and no scratch: rows
+    without a slot are 0, and the results are those of the current stream."""
+    T, H = 3000, 4
+    x = torch.randn(T, H, 128, device="cuda")
+    cache = torch.zeros(T // 16 + 1, H, 16 * 144, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(T, dtype=I32, device="cuda")
+    slots[::3] = -1
+    B.diffattn_kv4_append(x, 2 * x, slots, cache)
+    want = B.diffattn_kv4_read(cache, slots)
+    pos = torch.arange(T, dtype=I32, device="cuda")
+    f, w = torch.rand(64, device="cuda"), torch.rand(128, device="cuda")
+    grads = B.diffattn_qk_norm_rope_bwd(x, x, x, x, pos, f, q_weight=w, k_weight=w)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        junk = torch.full((T, H, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        del junk                     # its memory may be what the next call gets
+        got = B.diffattn_kv4_read(cache, slots, stream=s)
+        g2 = B.diffattn_qk_norm_rope_bwd(x, x, x, x, pos, f, q_weight=w, k_weight=w,
+                                         stream=s.cuda_stream)
+        s.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert not got[0][::3].any()
+        for name in grads:
+            assert torch.equal(g2[name], grads[name]), name
+        torch.cuda.synchronize()
+
+
 def test_cache_no_tokens(B):
     cache = torch.zeros(2, 1, 16 * 144, dtype=torch.uint8, device="cuda")
     x = torch.ones(0, 1, 128, device="cuda")

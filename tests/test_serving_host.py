@@ -133,6 +133,14 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(b):
                               cache)
     with pytest.raises(TypeError, match="v must be"):
         b.diffattn_kv4_append(rows, rows.float(), slots, cache)
+    with pytest.raises(TypeError, match="dev_status"):
+        b.diffattn_kv4_append(rows, rows, slots, cache, dev_status=slots.to(torch.uint8))
+    with pytest.raises(TypeError, match="k must be a tensor"):
+        b.diffattn_kv4_append(None, rows, slots, cache)
+    with pytest.raises(TypeError, match="dtype"):
+        b.diffattn_kv4_read(cache, slots, dtype=torch.float16)
+    with pytest.raises(ValueError, match="out of range"):
+        b.diffattn_page_plan(slots, slots, torch.zeros(5, 2, **i32), slots, slots[:1], 16, 1 << 40)
     with pytest.raises(ValueError, match="page_size"):
         b.diffattn_kv4_read(torch.zeros(3, 2, 100, dtype=torch.uint8), slots)
     q = torch.zeros(5, 4, 128, dtype=torch.bfloat16)

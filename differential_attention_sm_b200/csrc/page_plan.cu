@@ -12,10 +12,11 @@
 // Bound by latency: a step of 64 requests moves 2 KB.  One CTA does the sums
 // and all state, a row of requests per pass, and with few slot rows also writes
 // those and the new table entries, since a thread holds what its request
-// needs.  With many (prompts), it leaves each request's depth in the stack in
-// the workspace, and a second kernel writes rows and entries with all SMs.
-// Measured: 64 requests 2.6 us; 517 requests with 268k slot rows 8.6 us (29 us
-// by one CTA).
+// needs.  With many (prompts), all SMs write rows and entries: each CTA adds up
+// the requests itself, or, with more than it keeps or with outputs in place, a
+// second kernel takes them from the first's outputs and the workspace.
+// Measured: 64 requests 2.6 us; 517 requests with 268k slot rows 6.8 us (29 us
+// by one CTA, 8.5 by two kernels).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -85,52 +86,92 @@ __device__ __forceinline__ int slot_of(const PlanArgs& a, int page, int pos, boo
   return (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
+__device__ __forceinline__ int free_pages_of(const PlanArgs& a) {
+  const int n = *a.count;
+  return n < 0 ? 0 : (n > a.n_pages ? a.n_pages : n);
+}
+__device__ __forceinline__ int clamped(long long x) { return (int)(x < INT_MAX ? x : INT_MAX); }
+
+// What request r gets; the block's threads take a row of requests together.
+struct Share {
+  bool live, ok;
+  int n, len, old, need;
+  long long at, end;  // slot rows [at, end)
+  long long upto;     // pages asked for by it and those before
+};
+__device__ __forceinline__ Share share_of(const PlanArgs& a, int r, int free0, long long* sh,
+                                          long long& tok_base, long long& need_base) {
+  const int ps = 1 << a.page_shift;
+  Share s;
+  s.live = r < a.requests;
+  s.n = s.live ? max(a.new_lens[r], 0) : 0;
+  s.len = s.live ? max(a.lens[r], 0) : 0;
+  long long total;
+  s.end = tok_base + block_scan(s.n, sh, total);
+  tok_base += total;
+  s.at = s.end - s.n;
+  const long long after = (long long)s.len + s.n;
+  const bool fits = s.live && after <= (long long)a.max_pages << a.page_shift &&
+                    (s.n == 0 || s.end <= a.n_slots);
+  s.old = fits ? (int)(((long long)s.len + ps - 1) >> a.page_shift) : 0;
+  s.need = fits ? (int)((after + ps - 1) >> a.page_shift) - s.old : 0;
+  s.upto = need_base + block_scan(s.need, sh, total);
+  need_base += total;
+  s.ok = fits && (s.need == 0 || s.upto <= free0);
+  return s;
+}
+// The request's outputs; `taken`: the most pages a served request reaches down to.
+__device__ __forceinline__ void put_share(const PlanArgs& a, int r, const Share& s, int& taken,
+                                          bool& refused) {
+  if (s.ok && s.need) taken = max(taken, (int)s.upto);
+  refused |= s.live && !s.ok;
+  if (!s.live) return;
+  a.offsets[r] = clamped(s.at);
+  if (r == a.requests - 1) a.offsets[r + 1] = clamped(s.end);
+  a.served[r] = s.ok ? 1 : 0;
+  a.lens_out[r] = s.ok ? s.len + s.n : s.len;
+}
+// The pages left, and what went wrong; the whole block calls it.
+__device__ __forceinline__ void put_count(const PlanArgs& a, int free0, int taken, bool refused,
+                                          long long* sh) {
+  taken = __reduce_max_sync(0xffffffffu, taken);
+  __syncthreads();
+  int* top = reinterpret_cast<int*>(sh);
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = taken;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, top[w]);
+    *a.count_out = free0 - taken;
+  }
+  if (refused) report(a.dev_status, DA_ERR_CACHE_FULL);
+}
+
 // `with_slots`: this launch writes the slot rows and table entries too.
 __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, int with_slots) {
   __shared__ long long sh[33];
   let_next_start();
   after_previous();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int ps = 1 << a.page_shift;
-  int free0 = *a.count;
-  free0 = free0 < 0 ? 0 : (free0 > a.n_pages ? a.n_pages : free0);
-  const long long room = (long long)a.max_pages << a.page_shift;
+  const int free0 = free_pages_of(a);
   long long tok_base = 0, need_base = 0;
-  int taken = 0;         // the most pages that a served request reaches down to
+  int taken = 0;
   bool refused = false, bad = false;
   for (int base = 0; base < a.requests; base += (int)blockDim.x) {
     const int r = base + tid;
-    const bool live = r < a.requests;
-    int n = live ? a.new_lens[r] : 0;
-    n = n < 0 ? 0 : n;
-    int len = live ? a.lens[r] : 0;
-    len = len < 0 ? 0 : len;
-    long long tok_total, need_total;
-    const long long tok_end = tok_base + block_scan(n, sh, tok_total);
-    const long long tok_at = tok_end - n;
-    const long long after = (long long)len + n;
-    const bool fits = live && after <= room && (n == 0 || tok_end <= a.n_slots);
-    const int old = fits ? (int)(((long long)len + ps - 1) >> a.page_shift) : 0;
-    const int need = fits ? (int)((after + ps - 1) >> a.page_shift) - old : 0;
-    const long long upto = need_base + block_scan(need, sh, need_total);
-    const bool ok = fits && (need == 0 || upto <= free0);
-    if (ok && need) taken = max(taken, (int)upto);
-    refused |= live && !ok;
-    if (live) {
-      a.offsets[r] = (int)(tok_at < INT_MAX ? tok_at : INT_MAX);
-      if (r == a.requests - 1) a.offsets[r + 1] = (int)(tok_end < INT_MAX ? tok_end : INT_MAX);
-      a.served[r] = ok ? 1 : 0;
-      a.lens_out[r] = ok ? (int)after : len;
-      if (!with_slots) a.depth[r] = ok && need ? (int)(free0 - upto + need) : 0;
-    }
+    const Share s = share_of(a, r, free0, sh, tok_base, need_base);
+    put_share(a, r, s, taken, refused);
+    if (s.live && !with_slots) a.depth[r] = s.ok && s.need ? (int)(free0 - s.upto + s.need) : 0;
+    const int len = s.len, old = s.old;
+    const long long tok_at = s.at;
+    const bool ok = s.ok;
     // New table entries and slot rows: a thread writes its own request's when
     // they are few, else its whole warp does, one request at a time.
-    const int depth = (int)(upto - need);
-    const int rows = with_slots && live && tok_at < a.n_slots
-                         ? (int)(tok_end < a.n_slots ? n : a.n_slots - tok_at) : 0;
-    const int pages = with_slots && ok ? need : 0;
+    const int depth = (int)(s.upto - s.need);
+    const int rows = with_slots && s.live && tok_at < a.n_slots
+                         ? (int)(s.end < a.n_slots ? s.n : a.n_slots - tok_at) : 0;
+    const int pages = with_slots && ok ? s.need : 0;
     const bool many = pages > 2 || rows > 2;
-    int* row = a.table + (size_t)(live ? r : 0) * a.max_pages;
+    int* row = a.table + (size_t)(s.live ? r : 0) * a.max_pages;
     if (!many) {
       for (int j = 0; j < pages; ++j) row[old + j] = a.stack[free0 - 1 - (depth + j)];
       for (int j = 0; j < rows; ++j) {
@@ -168,8 +209,6 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
         a.positions[w_at + j] = pos;
       }
     }
-    tok_base += tok_total;
-    need_base += need_total;
   }
   if (with_slots) {  // rows behind the last token
     for (long long i = tok_base + tid; i < a.n_slots; i += blockDim.x) {
@@ -177,37 +216,18 @@ __global__ void __launch_bounds__(1024, 1) page_plan_kernel(const PlanArgs a, in
       a.positions[i] = 0;
     }
   }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, off));
-  __syncthreads();
-  int* top = reinterpret_cast<int*>(sh);
-  if (lane == 0) top[tid >> 5] = taken;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) taken = max(taken, top[w]);
-    *a.count_out = free0 - taken;
-  }
+  put_count(a, free0, taken, refused, sh);
   if (bad) report(a.dev_status, DA_ERR_PAGE);
-  if (refused) report(a.dev_status, DA_ERR_CACHE_FULL);
 }
 
-// Slot rows of a large step: a CTA finds the requests of its rows by bisection
-// over the offsets and, if they are few, keeps what it needs of them in shared
-// memory; a thread bisects those for each of its rows.  The row that begins a
-// new page writes its table entry: a new page's first position is a new token's.
-constexpr int kFillThreads = 256;
-constexpr int kFillRows = 1024;
-constexpr int kFillKeep = 1536;
+// Slot rows of a large step: each is bisected for its request.  The row that
+// begins a new page writes its table entry: a new page's first position is a
+// new token's.
+constexpr int kFillRows = 1024;  // of a CTA
 
 struct Request {
   int offset, len, depth;  // the first new page lies below stack[depth]; < 0: not served
 };
-
-__device__ __forceinline__ Request request_of(const PlanArgs& a, int r) {
-  const int n = a.new_lens[r], ok = a.served[r];
-  return {a.offsets[r], (int)((unsigned)a.lens_out[r] - (unsigned)(ok && n > 0 ? n : 0)),
-          ok ? a.depth[r] : -1};
-}
 
 // Last r in [lo, hi] whose offset is at most i.
 template <typename F>
@@ -218,6 +238,78 @@ __device__ __forceinline__ int upper_request(F offset, int lo, int hi, int i) {
     else hi = mid - 1;
   }
   return lo;
+}
+
+__device__ __forceinline__ int fill_row(const PlanArgs& a, int i, int r, const Request& q,
+                                        int& pos, bool& bad) {
+  const int mask = (1 << a.page_shift) - 1;
+  pos = (int)((unsigned)q.len + (unsigned)(i - q.offset));
+  if (q.depth < 0) return -1;
+  const int blk = pos >> a.page_shift;
+  const int old = (int)(((unsigned)q.len + (unsigned)mask) >> a.page_shift);
+  int* entry = a.table + (size_t)r * a.max_pages + blk;
+  int page;
+  if (blk < old) {
+    page = *entry;
+  } else {
+    page = a.stack[q.depth - 1 - (blk - old)];
+    if ((pos & mask) == 0) *entry = page;
+  }
+  return slot_of(a, page, pos, bad);
+}
+
+// One launch for large steps of up to kWideRequests requests: every CTA adds up
+// the requests itself (1 us) and keeps them in shared memory for its rows; the
+// first writes the requests' outputs.  Those must not be the inputs, which the
+// other CTAs may still read.
+constexpr int kWideRequests = 2048;
+
+__global__ void __launch_bounds__(1024) page_plan_wide_kernel(const PlanArgs a) {
+  __shared__ long long sh[33];
+  __shared__ Request keep[kWideRequests];
+  let_next_start();
+  after_previous();
+  const int free0 = free_pages_of(a);
+  long long tok_base = 0, need_base = 0;
+  int taken = 0;
+  bool refused = false, bad = false;
+  for (int base = 0; base < a.requests; base += (int)blockDim.x) {
+    const int r = base + (int)threadIdx.x;
+    const Share s = share_of(a, r, free0, sh, tok_base, need_base);
+    if (s.live)
+      keep[r] = {clamped(s.at), s.len,
+                 !s.ok ? -1 : s.need ? (int)(free0 - s.upto + s.need) : 0};
+    if (blockIdx.x == 0) put_share(a, r, s, taken, refused);
+  }
+  if (blockIdx.x == 0) put_count(a, free0, taken, refused, sh);
+  __syncthreads();
+  const int first = (int)blockIdx.x * kFillRows;
+  const int last = min(first + kFillRows, a.n_slots) - 1;
+  auto offset = [&](int r) { return keep[r].offset; };
+  const int lo = upper_request(offset, 0, a.requests - 1, first);
+  const int hi = upper_request(offset, lo, a.requests - 1, last);
+  for (int i = first + (int)threadIdx.x; i <= last; i += (int)blockDim.x) {
+    int slot = -1, pos = 0;
+    if (i < tok_base) {
+      const int r = upper_request(offset, lo, hi, i);
+      slot = fill_row(a, i, r, keep[r], pos, bad);
+    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
+  }
+  if (bad) report(a.dev_status, DA_ERR_PAGE);
+}
+
+// The same rows after page_plan_kernel, for more requests or outputs in place: a
+// CTA finds its requests in the written offsets and, if they are few, keeps
+// what it needs of them in shared memory.
+constexpr int kFillThreads = 256;
+constexpr int kFillKeep = 1536;
+
+__device__ __forceinline__ Request request_of(const PlanArgs& a, int r) {
+  const int n = a.new_lens[r], ok = a.served[r];
+  return {a.offsets[r], (int)((unsigned)a.lens_out[r] - (unsigned)(ok && n > 0 ? n : 0)),
+          ok ? a.depth[r] : -1};
 }
 
 __global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs a) {
@@ -237,28 +329,13 @@ __global__ void __launch_bounds__(kFillThreads) page_slots_kernel(const PlanArgs
     for (int r = lo + threadIdx.x; r <= hi; r += kFillThreads) keep[r - lo] = request_of(a, r);
   __syncthreads();
   const int total = a.offsets[a.requests];
-  const int mask = (1 << a.page_shift) - 1;
   bool bad = false;
   for (int i = first + threadIdx.x; i <= last; i += kFillThreads) {
     int slot = -1, pos = 0;
     if (i < total) {
       const int r = kept ? lo + upper_request([&](int k) { return keep[k].offset; }, 0, hi - lo, i)
                          : upper_request(global, lo, hi, i);
-      const Request q = kept ? keep[r - lo] : request_of(a, r);
-      pos = (int)((unsigned)q.len + (unsigned)(i - q.offset));
-      if (q.depth >= 0) {
-        const int blk = pos >> a.page_shift;
-        const int old = (int)(((unsigned)q.len + (unsigned)mask) >> a.page_shift);
-        int* entry = a.table + (size_t)r * a.max_pages + blk;
-        int page;
-        if (blk < old) {
-          page = *entry;
-        } else {
-          page = a.stack[q.depth - 1 - (blk - old)];
-          if ((pos & mask) == 0) *entry = page;
-        }
-        slot = slot_of(a, page, pos, bad);
-      }
+      slot = fill_row(a, i, r, kept ? keep[r - lo] : request_of(a, r), pos, bad);
     }
     a.slots[i] = slot;
     a.positions[i] = pos;
@@ -350,12 +427,13 @@ int check(int requests, int max_pages, int n_pages, int page_size) {
   return DA_OK;
 }
 
-// Whether the one CTA of the plan writes the slot rows itself: few rows, or few
-// for each request (a decode step with spare rows).  Measured (one CTA, two
-// kernels): 64 requests and 1024 rows 5.9 and 6.5 us, 2064 rows 9.2 and 6.7,
-// 12864 rows 26 and 7.1; 1500 requests and 6500 rows 7.3 and 9.
+// Whether the one CTA of the plan writes the slot rows itself: few of them for
+// each request (a decode step, with spare rows).  Measured (one CTA, all SMs):
+// 64 requests and 64 rows 2.6 and 3.6 us, 256 rows 2.9 and 3.8, 1024 rows 5.7
+// and 4.3, 12864 rows 27 and 4.1; 512 requests and 1024 rows 3.4 and 4.4; 1500
+// requests and 6500 rows 6.9 and 7.7.
 bool one_cta(int requests, int n_slots) {
-  return n_slots <= 16384 && n_slots <= 1024 + 4LL * requests;
+  return n_slots <= 16384 && n_slots <= 256 + 4LL * requests;
 }
 
 }  // namespace
@@ -401,14 +479,19 @@ extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, in
   a.depth = static_cast<int*>(workspace);
   a.dev_status = dev_status;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const dim3 fill((unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows));
+  if (need > 0 && requests <= da::kWideRequests && cache_lens_out != cache_lens &&
+      free_count_out != free_count)
+    return da::launch_after(da::page_plan_wide_kernel, fill, requests <= 512 ? 512 : 1024, 0, cs, a) ==
+                   cudaSuccess
+               ? DA_OK
+               : DA_ERR_CUDA;
   if (da::launch_after(da::page_plan_kernel, dim3(1), da::threads_for(requests), 0, cs, a,
                        (int)(need == 0)) != cudaSuccess)
     return DA_ERR_CUDA;
-  if (need > 0) {
-    const dim3 grid((unsigned)((n_slots + da::kFillRows - 1) / da::kFillRows));
-    if (da::launch_after(da::page_slots_kernel, grid, da::kFillThreads, 0, cs, a) != cudaSuccess)
-      return DA_ERR_CUDA;
-  }
+  if (need > 0 && da::launch_after(da::page_slots_kernel, fill, da::kFillThreads, 0, cs, a) !=
+                      cudaSuccess)
+    return DA_ERR_CUDA;
   return DA_OK;
 }
 

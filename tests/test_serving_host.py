@@ -36,8 +36,8 @@ def test_status_strings(b):
 
 def test_page_plan_refusals(b):
     inv, uns = b.DA_ERR_INVALID_ARG, b.DA_ERR_UNSUPPORTED
-    assert b.diffattn_page_plan_workspace_size(4, 1024) == 0
-    ws = b.diffattn_page_plan_workspace_size(4, 4097)
+    assert b.diffattn_page_plan_workspace_size(4, 272) == 0
+    ws = b.diffattn_page_plan_workspace_size(4, 273)
     assert ws > 0
     ok = [A] * 5 + [4, 8, 100, 64, 7] + [A] * 6 + [None, 0, None, None]
     refuses(b.load().diffattn_page_plan, ok, [
@@ -45,7 +45,7 @@ def test_page_plan_refusals(b):
         (5, 0, inv), (6, 0, inv), (7, 0, inv), (8, 0, inv), (9, -1, inv),
         (8, 48, uns), (8, 8, uns), (8, 2048, uns), (5, (1 << 16) + 1, uns),
         (7, 1 << 25, uns), (6, 1 << 25, uns), (9, (1 << 30) + 1, uns),
-        (9, 4097, b.DA_ERR_WORKSPACE), ((9, 16, 17), (4097, A, ws - 1), b.DA_ERR_WORKSPACE)])
+        (9, 273, b.DA_ERR_WORKSPACE), ((9, 16, 17), (273, A, ws - 1), b.DA_ERR_WORKSPACE)])
     ok = [A] * 5 + [4, 8, 100, 64, None, None]
     refuses(b.load().diffattn_page_release, ok, [
         *((i, None, inv) for i in range(5)), (5, 0, inv), (8, 24, uns)])

@@ -30,8 +30,9 @@
 // workspace; a second kernel joins them, subtracts, and normalises.
 //
 // Measured, 64 sequences of 32768 entries, 8 KV heads, 64 query heads (2.4 GB):
-// 376 to 415 us in bursts at 1965 MHz, 0.98 to 0.89 of the copy rate, 430 to
-// 445 us when the board's power limit sets the clock; the copies alone take 365.
+// 377 us in bursts at 1965 MHz, 0.98 of the copy rate (the copies alone 363);
+// 430 to 460 us when the board's power limit sets the clock.  V1, 16 x 8191 x
+// 32 heads (0.6 GB): 100 to 117 us.
 // A tile and head costs 238 instructions: 64 conversions, 64 multiplications
 // and 16 matrix instructions, which hold the former two up for 7 of their 8
 // clocks, make 285 of about 400 clocks of an SM quarter, where the memory

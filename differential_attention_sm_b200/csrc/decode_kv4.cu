@@ -57,9 +57,12 @@ constexpr int kD = 128;
 constexpr int kTiles = 4;  // of a stage
 constexpr int kStageTokens = kTiles * kKv4Tile;
 constexpr int kStageBytes = kTiles * kKv4TileBytes;
-constexpr int kWarps = 12;  // one CTA an SM: 3 of 4 warps took 104 us for 101 (V1, 16 x 8191)
+// Warps of a CTA, one CTA an SM (3 of 4 warps took 104 us for 101: V1, 16 x 8191).
+// Two column tiles need 235 registers a thread: 8 warps, where 12 with 168 spill
+// (32 sequences of 8192 entries, 80 query heads on 8: 84 us for 91; with one
+// tile 8 warps take 66 us for 63).
+__host__ __device__ constexpr int warps_of(int tiles) { return tiles == 1 ? 12 : 8; }
 constexpr int kRing = 2;
-constexpr int kCtasPerSm = 1;
 constexpr int kPlanSms = 148;      // fixed: the workspace size is the same on every device
 constexpr int kMinStages = 1;      // shortest run of a warp
 constexpr int kChunkHeads = 16;    // query heads that share one pass over the cache
@@ -91,7 +94,7 @@ struct Kv4Args {
   float eps, post_scale;
 };
 
-constexpr int kSmemBytes = kWarps * kRing * (kStageBytes + 16);
+__host__ __device__ constexpr int smem_of(int tiles) { return warps_of(tiles) * kRing * (kStageBytes + 16); }
 
 __device__ __forceinline__ void span_of(const Kv4Args& a, int b, int& lo, int& len) {
   const long long room = (long long)a.max_pages << a.page_shift;
@@ -317,8 +320,8 @@ __device__ __forceinline__ void tile_values(uint32_t at, uint32_t lane, uint32_t
 }
 
 template <int NT, bool kV1>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
-    kv4_decode_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(warps_of(NT) * 32, 1) kv4_decode_kernel(const Kv4Args a) {
+  constexpr int kWarps = warps_of(NT);
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t lane = threadIdx.x & 31u;
   const int warp = (int)(threadIdx.x >> 5);
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kRuns = kPlanSms * kCtasPerSm * kWarps;
+int runs_of(int cols) { return kPlanSms * warps_of(cols > 8 ? 2 : 1); }
 
 // Up to this many sequences the second kernel finds a unit's segments by adding
 // up the lengths before it, which costs no trip to what the first kernel wrote
@@ -754,7 +757,7 @@ constexpr int kRuns = kPlanSms * kCtasPerSm * kWarps;
 constexpr int kSumBatch = 256;
 
 size_t workspace_bytes_of(int batch, int units, int cols) {
-  const size_t slots = (size_t)batch * units + kRuns;
+  const size_t slots = (size_t)batch * units + runs_of(cols);
   return slots * cols * (kD + 2) * sizeof(float) +
          (batch > kSumBatch ? (size_t)batch * units * sizeof(int2) : 0);
 }
@@ -762,22 +765,22 @@ size_t workspace_bytes_of(int batch, int units, int cols) {
 int chunks_of(int group) { return (group + kChunkHeads - 1) / kChunkHeads; }
 
 cudaError_t launch(Kv4Args& a, void* workspace, cudaStream_t stream) {
-  a.runs = kRuns;
+  a.runs = runs_of(a.cols);
   const size_t slots = (size_t)a.batch * a.heads * a.chunks + a.runs;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + slots * a.cols * kD;
   a.spans = a.batch > kSumBatch ? reinterpret_cast<int2*>(a.part_ml + slots * a.cols * 2) : nullptr;
-  const unsigned grid = (unsigned)(a.runs / kWarps);
-  auto run = [&](auto kernel) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmemBytes);
+  auto run = [&](auto kernel, int tiles) -> cudaError_t {
+    const int smem = smem_of(tiles);
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(grid), kWarps * 32, kSmemBytes, stream, a);
+    return launch_after(kernel, dim3(kPlanSms), warps_of(tiles) * 32, smem, stream, a);
   };
   cudaError_t e;
-  if (a.v1) e = run(kv4_decode_kernel<1, true>);
-  else if (a.cols <= 8) e = run(kv4_decode_kernel<1, false>);
-  else e = run(kv4_decode_kernel<2, false>);
+  if (a.v1) e = run(kv4_decode_kernel<1, true>, 1);
+  else if (a.cols <= 8) e = run(kv4_decode_kernel<1, false>, 1);
+  else e = run(kv4_decode_kernel<2, false>, 2);
   if (e != cudaSuccess) return e;
   return launch_after(kv4_combine_kernel, dim3((unsigned)a.batch * (unsigned)a.out_heads),
                       kCombineWarps * 32, 0, stream, a);

@@ -113,7 +113,8 @@ __device__ __forceinline__ uint2 codes_of(const Block<__nv_bfloat16>& b, float s
   unpack(b, x);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  const uint64_t inv2 = f2pack(inv, inv), up = f2pack(3072.f, 3072.f), down = f2pack(-3072.f, -3072.f);
+  constexpr float kAway = 1.5f * 2048.0f;  // its neighbours are 2^-12 apart
+  const uint64_t inv2 = f2pack(inv, inv), up = f2pack(kAway, kAway), down = f2pack(-kAway, -kAway);
   float y[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {  // to multiples of 2^-12

@@ -47,6 +47,7 @@
 #include "diffattn.h"
 #include "kernels.h"
 #include "kv4.cuh"
+#include "kv4_index.h"
 #include "launch.cuh"
 #include "ptx.cuh"
 
@@ -67,8 +68,6 @@ constexpr int kPlanSms = 148;      // fixed: the workspace size is the same on e
 constexpr int kMinStages = 1;      // shortest run of a warp
 constexpr int kChunkHeads = 16;    // query heads that share one pass over the cache
 constexpr float kNoMax = -3.0e38f;
-constexpr uint32_t kNoTile = 0xFFFFFFFFu;   // of no use to the segment
-constexpr uint32_t kBadTile = 0xFFFFFFFEu;  // on a page out of range
 constexpr float kShift = 5.0f;    // p = 2^(s - m + kShift)
 constexpr float kRaise = 10.0f;   // m is raised when a score passes m + kRaise
 
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) kv4_decode_kernel(const 
     // Bit l: the tiles of lanes l and l + 1 are neighbours in memory.
     auto joined = [&](uint32_t mine) {
       const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
-      return __ballot_sync(0xffffffffu, next == mine + 1u && next < kBadTile);
+      return __ballot_sync(0xffffffffu, tiles_joined(mine, next));
     };
     uint32_t tile = tile_of((int)lane), ahead = tile_of(32 + (int)lane);
     uint32_t join = joined(tile);

@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
   if (a.spans && n_b > 0) {
     const int2 v = a.spans[(size_t)b * units + unit];
     w0 = v.x, n = v.y;
+    bound_span(w0, n, a.runs);
   }
   const long long slot0 = (long long)b * units + unit + w0;
   const float* ml = a.part_ml + (slot0 * a.cols + col) * 2;

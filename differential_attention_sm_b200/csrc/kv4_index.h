@@ -23,4 +23,13 @@ DA_INDEX_FN bool tiles_joined(uint32_t mine, uint32_t next) {
   return mine < kBadTile && next < kBadTile && next == mine + 1u;
 }
 
+// Runs [first, first + count) of a unit, as they were written down, cut to the
+// runs that there are.  A warp whose wait timed out leaves without writing its
+// units' spans: what lies there then is whatever the scratch held, and the
+// second kernel, which still runs, must not read outside the scratch for it.
+DA_INDEX_FN void bound_span(int& first, int& count, int runs) {
+  first = first < 0 ? 0 : (first > runs ? runs : first);
+  count = count < 0 ? 0 : (count > runs - first ? runs - first : count);
+}
+
 }  // namespace da

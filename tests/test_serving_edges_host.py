@@ -17,7 +17,9 @@ def index(tmp_path_factory):
     src = d / "index.cpp"
     src.write_text('#include "kv4_index.h"\n'
                    'extern "C" int joined(unsigned a, unsigned b) '
-                   '{ return da::tiles_joined(a, b); }\n')
+                   '{ return da::tiles_joined(a, b); }\n'
+                   'extern "C" void span(int* v, int runs) '
+                   '{ da::bound_span(v[0], v[1], runs); }\n')
     so = d / "index.so"
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I" + CSRC, str(src), "-o",
                     str(so)], check=True)
@@ -36,3 +38,19 @@ def test_only_tiles_of_the_cache_are_joined(index):
         for other in (0, 1, BAD_TILE - 1, BAD_TILE, NO_TILE):
             assert not index.joined(none, other), (none, other)
             assert not index.joined(other, none), (other, none)
+
+
+def test_spans_of_a_unit_stay_within_the_scratch(index):
+    """Spans that no warp wrote (its wait timed out) hold anything.  The scratch
+    has a slot for each unit and one for each run: slot unit + first + i, with
+    i below count, is inside it."""
+    edge = [-2 ** 31, -2 ** 31 + 1, -1, 0, 1, 2, 1183, 1184, 1185, 1775, 1776, 1777, 2 ** 30,
+            2 ** 31 - 2, 2 ** 31 - 1]
+    for runs in (1184, 1776):
+        for first in edge:
+            for count in edge:
+                v = (ctypes.c_int * 2)(first, count)
+                index.span(v, runs)
+                assert v[0] >= 0 and v[1] >= 0 and v[0] + v[1] <= runs, (first, count, list(v))
+                if 0 <= first and 0 <= count and first + count <= runs:
+                    assert list(v) == [first, count]

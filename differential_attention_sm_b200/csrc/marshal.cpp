@@ -465,6 +465,8 @@ PyObject* decode_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Cache c = kv4_cache(cache);
   if (v1 && c.heads != H)
     refuse(PyExc_ValueError, "cache holds %d heads, q %lld", c.heads, (long long)H);
+  if (v1 && d % 2)  // a head's width is passed as that of its two branches
+    refuse(PyExc_ValueError, "q's width must be that of two branches, not %lld", (long long)d);
   need("block_table", table, at::kInt);
   if (table.dim() != 2 || table.size(0) != B)
     refuse(PyExc_ValueError, "block_table must be [%lld, max_pages], not %s", (long long)B,

@@ -1,14 +1,25 @@
 """Host side of the serving operators at their edges: the decode's index rules,
-compiled from the kernel's own header by the host compiler.  No device."""
+compiled from the kernel's own header by the host compiler, and calls that are
+refused.  No device."""
 import ctypes
 import os
 import subprocess
 
 import pytest
+import torch
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "differential_attention_sm_b200", "csrc")
 NO_TILE, BAD_TILE = 0xFFFFFFFF, 0xFFFFFFFE
+
+
+@pytest.fixture(scope="module")
+def b():
+    from differential_attention_sm_b200 import build
+    build.build()
+    from differential_attention_sm_b200 import binding
+    binding.load()
+    return binding
 
 
 @pytest.fixture(scope="module")
@@ -34,7 +45,8 @@ def test_only_tiles_of_the_cache_are_joined(index):
     for mine in (0, 1, 7, 0x7FFFFFFF, BAD_TILE - 2):
         assert index.joined(mine, mine + 1)
         assert not index.joined(mine, mine) and not index.joined(mine, mine + 2)
-    for none in (NO_TILE, BAD_TILE):
+    for none in (A = 0x10000   # 16-byte aligned fake device address
+NO_TILE, BAD_TILE):
         for other in (0, 1, BAD_TILE - 1, BAD_TILE, NO_TILE):
             assert not index.joined(none, other), (none, other)
             assert not index.joined(other, none), (other, none)
@@ -54,3 +66,14 @@ def test_spans_of_a_unit_stay_within_the_scratch(index):
                 assert v[0] >= 0 and v[1] >= 0 and v[0] + v[1] <= runs, (first, count, list(v))
                 if 0 <= first and 0 <= count and first + count <= runs:
                     assert list(v) == [first, count]
+
+
+def test_v1_decode_refuses_an_odd_width(b):
+    """Half of it would pass for a branch, and the rows for rows of 128."""
+    i32 = dict(dtype=torch.int32)
+    cache = torch.zeros(3, 4, 16 * 144, dtype=torch.uint8)
+    for width in (127, 129):
+        q = torch.zeros(5, 4, width, dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="width"):
+            b.diffattn_v1_decode_kv4(q, cache, torch.zeros(5, 2, **i32), torch.zeros(5, **i32),
+                                     torch.zeros(4))

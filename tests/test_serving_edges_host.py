@@ -45,8 +45,7 @@ def test_only_tiles_of_the_cache_are_joined(index):
     for mine in (0, 1, 7, 0x7FFFFFFF, BAD_TILE - 2):
         assert index.joined(mine, mine + 1)
         assert not index.joined(mine, mine) and not index.joined(mine, mine + 2)
-    for none in (A = 0x10000   # 16-byte aligned fake device address
-NO_TILE, BAD_TILE):
+    for none in (NO_TILE, BAD_TILE):
         for other in (0, 1, BAD_TILE - 1, BAD_TILE, NO_TILE):
             assert not index.joined(none, other), (none, other)
             assert not index.joined(other, none), (other, none)

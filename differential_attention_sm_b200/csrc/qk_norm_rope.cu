@@ -340,23 +340,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_kernel(cons
 }
 
 // Backward.  CTAs walk over batches of tokens as above and keep the weights'
-// gradient of their own rows in registers (fp32: a thread adds a few hundred
-// rows at most); each writes one row of sums, and the second kernel adds those
-// in 64 bits.  The order depends on the sizes alone.
+// gradient of their own rows in registers, in fp32 for up to kFoldRows rows of a
+// thread.  With more (kMany; 1.2 million rows of 128), a warp adds those up in 64
+// bits in shared memory and begins anew, so that the error does not grow with
+// the rows; 8 million rows of 128 take 1.71 ms with it and 1.66 without, and
+// 16384 tokens of 64 heads of 64, which need none, 117 and 116 us.  Each CTA writes
+// one row of sums, and the second kernel adds those in 64 bits.  The order depends
+// on the sizes alone.
 constexpr int kBwdDepth = 2;  // rows of a thread in shared memory (3: 114 us for 110)
+constexpr int kFoldRows = 128;
 template <typename T>
 struct BwdSmem {
   float cs[2][kAngles], sn[2][kAngles];
   union {
     uint4 ring[kBwdDepth][sizeof(T) + 4][kThreads];  // words of x, then of dy
-    float sums[kThreads / 32][2 * 256];
+    float sums[kThreads / 32][2 * 256];              // the warps' last rows
   };
+  // and with kMany double [kThreads / 32][2 * d] behind it: their rows before those
 };
+template <typename T>
+constexpr int bwd_smem_of(int d, bool many) {
+  return (int)sizeof(BwdSmem<T>) + (many ? kThreads / 32 * 2 * d * (int)sizeof(double) : 0);
+}
 
-template <typename T, int G, bool kInterleaved>
+template <typename T, int G, bool kInterleaved, bool kMany>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   BwdSmem<T>& sh = *reinterpret_cast<BwdSmem<T>*>(smem);
+  double* const folded = reinterpret_cast<double*>(smem + sizeof(BwdSmem<T>));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   let_next_start();
   after_previous();
   const int j = threadIdx.x % G, g = threadIdx.x / G;
@@ -408,6 +420,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(
   float acc[2][16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+  // The sums of the warp's groups, in every lane.
+  auto add_groups = [&] {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int off = G; off < 32; off <<= 1)
+          acc[k][i] += __shfl_xor_sync(0xffffffffu, acc[k][i], off);
+  };
+  int rows = 0;         // in acc
+  bool more = false;    // `folded` holds some
+  auto fold = [&] {
+    add_groups();
+    if (lane < G && in_row) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          double* p = folded + (warp * 2 + k) * a.d + (half ? o1 : o0);
+          double v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = more ? p[i] : 0.0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = v[i] + (double)acc[k][8 * half + i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
+    rows = 0;
+    more = true;
+  };
   angles(a, (int)blockIdx.x << a.tok_log2, sh.cs[0], sh.sn[0]);
   int buf = 0;
   for (int batch = blockIdx.x; batch < batches; batch += gridDim.x, buf ^= 1) {
@@ -480,19 +524,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(
         store8(p + o0, x);
         store8(p + o1, x + 8);
       }
+      if (kMany && ++rows == kFoldRows) fold();  // all lanes: the CTA's groups take the same turns
     }
   }
   copy_wait<0>();
   __syncthreads();  // the ring's place is taken by the sums
   // Sum over the warp's groups, then over the warps.
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int off = G; off < 32; off <<= 1)
-        acc[k][i] += __shfl_xor_sync(0xffffffffu, acc[k][i], off);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  add_groups();
   if (lane < G && in_row) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -505,6 +543,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) qk_norm_rope_bwd_kernel(
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) v += sh.sums[w][i];
+    if (kMany && more) {
+      double all = v;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) all += folded[w * 2 * a.d + i];
+      v = (float)all;
+    }
     a.partial[(size_t)blockIdx.x * 2 * a.d + i] = v;
   }
 }
@@ -721,12 +765,20 @@ extern "C" int diffattn_qk_norm_rope_bwd(
   a.tok_log2 = da::batch_log2(tokens, heads, lanes, rot_dim, 4);
   const int batches = (int)(((long long)tokens + (1 << a.tok_log2) - 1) >> a.tok_log2);
   const int ctas = batches < da::kBwdCtas ? batches : da::kBwdCtas;
+  const int per_tok = (da::kThreads / lanes) >> a.tok_log2;
+  const long long rows = (long long)((batches + ctas - 1) / ctas) * ((heads + per_tok - 1) / per_tok);
   cudaError_t e = cudaSuccess;
+  auto run = [&](auto t, auto g, auto il, auto many) {
+    auto kernel = da::qk_norm_rope_bwd_kernel<decltype(t), decltype(g)::value,
+                                              decltype(il)::value, decltype(many)::value>;
+    const int bytes = da::bwd_smem_of<decltype(t)>(head_dim, decltype(many)::value);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             da::bwd_smem_of<decltype(t)>(256, decltype(many)::value));
+    if (e == cudaSuccess) e = da::launch_after(kernel, dim3(ctas), da::kThreads, bytes, cs, a);
+  };
   da::dispatch(dtype, lanes, interleaved != 0, [&](auto t, auto g, auto il) {
-    auto kernel = da::qk_norm_rope_bwd_kernel<decltype(t), decltype(g)::value, decltype(il)::value>;
-    constexpr int kBytes = (int)sizeof(da::BwdSmem<decltype(t)>);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e == cudaSuccess) e = da::launch_after(kernel, dim3(ctas), da::kThreads, kBytes, cs, a);
+    if (rows > da::kFoldRows) run(t, g, il, std::true_type{});
+    else run(t, g, il, std::false_type{});
   });
   if (e != cudaSuccess) return DA_ERR_CUDA;
   if ((dq_weight || dk_weight) &&

@@ -32,3 +32,24 @@ def test_window_before_the_first_tile_of_the_cache(B, form, tile):
     table[0, :n_tiles] = [n_tiles - tile + j for j in range(tile)] + list(range(n_tiles - tile))
     assert sorted(table[0, :n_tiles]) == list(range(n_tiles))
     check_decode(B, cache, table, lens, q, [0.4], form, window)
+
+
+# ---- norm: gradients of the weights ------------------------------------------------
+def test_weight_gradient_of_many_rows(B):
+    """Sums of rows that all round the same way: 1023 of a thread, each 1 + 0.45
+    * 2^-14, which a running fp32 sum above 512 cuts to 1.  The bound counts 22
+    half steps of a term, 128 of the adds that are in fp32 and 6 behind them,
+    however many rows there are; a chain of them all is off by 205."""
+    H, d = 32, 256
+    T = 1023 * 148 * 2 * 16 // H           # two CTAs an SM, 16 rows of a CTA at a time
+    x = torch.ones(T, H, d, dtype=torch.bfloat16, device="cuda")
+    c = float(np.float32(1 + 0.45 * 2.0 ** -14))
+    dy = torch.full((T, H, d), c, device="cuda")
+    w = torch.ones(d, device="cuda")
+    got = B.diffattn_qk_norm_rope_bwd(x, None, dy, None, None, None, q_weight=w, norm_eps=0.0)
+    want = T * H * c
+    worst = float((got["dq_weight"].double() - want).abs().max())
+    assert worst <= (22 + 128 + 6) * 2.0 ** -24 * want, worst / want * 2.0 ** 24
+    # all of the gradient lies along x: w dy - x mean(x w dy) is 0 but for the
+    # rounding of a sum of 256 and of the root
+    assert float(got["dq"].abs().max()) <= 64 * 2.0 ** -24 * c

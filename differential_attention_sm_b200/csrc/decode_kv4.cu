@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) kv4_decode_kernel(const 
   }
   __syncwarp();
   after_previous();
-  let_next_start();  // not sooner: the second kernel reads the lengths before its own wait
+  let_next_start();  // not sooner: kv4_combine_kernel reads the lengths before its own wait
 
   const int units = a.heads * a.chunks;  // of one sequence
   long long before, total;
@@ -654,6 +654,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
     unit = kvh * a.chunks + at / kChunkHeads;
     col = at % kChunkHeads;
   }
+  // The lengths (a.lens) are read before after_previous(), which hides the sums
+  // behind the end of the decode.  Whatever wrote them is done: only
+  // kv4_decode_kernel is launched before this kernel, it lets this one start
+  // behind its own wait, and it does not write them.  It has to stay so.
   const int units = a.heads * a.chunks;
   const int n_b = stages_of(a, b);
   int w0 = 0, n = 0;  // first run, and segments

@@ -227,10 +227,13 @@ __device__ __forceinline__ int clc_response(const void* resp) {
 // Everything before this kernel in the stream is done and visible.  Comes
 // before a kernel's first access to global memory.  (No ld.global.nc in such a
 // kernel of what the one before may write: it changes while this one lives.)
+// One kernel reads sooner: kv4_combine_kernel the cache's lengths, which is sound
+// because the only kernel launched before it signals behind its own wait.
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-// The next kernel's CTAs may be placed once all CTAs of this one have come here.
+// The next kernel's CTAs may be placed once all CTAs of this one have come here:
+// before after_previous() the next one may run beside the one before this one.
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

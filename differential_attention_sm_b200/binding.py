@@ -684,7 +684,8 @@ def diffattn_page_plan(new_lens, cache_lens, block_table, free_pages, free_count
     [1] are free.  Returns a dict: slots, positions [n_slots], offsets
     [R + 1], served, cache_lens [R], free_count [1] (int32).  `out`, such a
     dict, is written instead of new tensors; its cache_lens and free_count
-    may be the arguments themselves."""
+    may be the arguments themselves.  Without that, what follows (a release,
+    the next plan) takes the returned cache_lens and free_count."""
     return (_marshal or _serving()).page_plan(
         new_lens, cache_lens, block_table, free_pages, free_count, page_size, n_slots, out,
         workspace, dev_status, stream)

@@ -472,8 +472,10 @@ DA_API size_t diffattn_kv4_page_bytes(int n_kv_heads, int head_dim, int page_siz
  *                   rows; workspace may be NULL then)
  * Up to 65536 requests and 2^30 slot rows.  DA_ERR_CACHE_FULL goes to
  * dev_status if a request was not served, DA_ERR_PAGE if a token would lie on
- * a page out of range (its slot is -1).  The result depends on the arguments' values alone, and a
- * call repeated with the same ones writes the same. */
+ * a page out of range (its slot is -1).  The result depends on the arguments'
+ * values alone, and a call repeated with the same ones writes the same: a step
+ * that goes on from here (a release, the next plan) has to take cache_lens_out
+ * and free_count_out, or the pages handed out here count as free again. */
 DA_API size_t diffattn_page_plan_workspace_size(int requests, int n_slots);
 DA_API int diffattn_page_plan(const int* new_lens, const int* cache_lens, int* block_table,
                               const int* free_pages, const int* free_count, int requests,

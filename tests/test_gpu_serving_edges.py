@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import readme_step
 from test_gpu_serving import check_decode, decode_state
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,8 @@ def test_weight_gradient_of_many_rows(B):
     # all of the gradient lies along x: w dy - x mean(x w dy) is 0 but for the
     # rounding of a sum of 256 and of the root
     assert float(got["dq"].abs().max()) <= 64 * 2.0 ** -24 * c
+
+
+# ---- the step that the documents show ----------------------------------------------
+def test_readme_step_keeps_the_page_pool(B):
+    readme_step.run(B, "cuda")

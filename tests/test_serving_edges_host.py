@@ -8,6 +8,9 @@ import subprocess
 import pytest
 import torch
 
+import readme_step
+import serving_reference as R
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "differential_attention_sm_b200", "csrc")
 NO_TILE, BAD_TILE = 0xFFFFFFFF, 0xFFFFFFFE
@@ -76,3 +79,42 @@ def test_v1_decode_refuses_an_odd_width(b):
         with pytest.raises(ValueError, match="width"):
             b.diffattn_v1_decode_kv4(q, cache, torch.zeros(5, 2, **i32), torch.zeros(5, **i32),
                                      torch.zeros(4))
+
+
+# ---- the step that the documents show ----------------------------------------------
+class Definitions:
+    """The calls of a serving step by their definitions, on the CPU."""
+
+    @staticmethod
+    def diffattn_page_plan(new, lens, table, stack, count, page, n_slots):
+        r = R.page_plan(new.numpy(), lens.numpy(), table.numpy(), stack.numpy(), int(count), page,
+                        n_slots)
+        table.copy_(torch.as_tensor(r.pop("block_table")))
+        return {k: torch.as_tensor(v).to(torch.int32) for k, v in r.items()}
+
+    @staticmethod
+    def diffattn_qk_norm_rope(q, k, positions, inv_freq, *, q_weight, k_weight):
+        assert len(positions) == len(q)
+        return q, k
+
+    @staticmethod
+    def diffattn_kv4_append(k, v, slots, cache):
+        assert len(slots) == len(k)
+
+    @staticmethod
+    def diffattn_v2_decode_kv4(q, cache, table, lens, lam):
+        return torch.zeros(q.shape[0], q.shape[1] // 2, 128)
+
+    @staticmethod
+    def diffattn_page_release(release, lens, table, stack, count, page):
+        for r in range(len(release)):
+            for j in range(-(-int(lens[r]) // page) if release[r] else 0):
+                stack[int(count)] = table[r, j]
+                table[r, j] = -1
+                count += 1
+            if release[r]:
+                lens[r] = 0
+
+
+def test_readme_step_keeps_the_page_pool():
+    readme_step.run(Definitions, "cpu")

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import readme_step
-from test_gpu_serving import check_decode, decode_state
+import serving_reference as R
+from test_gpu_serving import check_decode, decode_state, dev, np64, within
 
 pytestmark = pytest.mark.gpu
 
@@ -33,6 +34,33 @@ def test_window_before_the_first_tile_of_the_cache(B, form, tile):
     table[0, :n_tiles] = [n_tiles - tile + j for j in range(tile)] + list(range(n_tiles - tile))
     assert sorted(table[0, :n_tiles]) == list(range(n_tiles))
     check_decode(B, cache, table, lens, q, [0.4], form, window)
+
+
+# ---- norm: infinities -----------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 0), (64, 32), (128, 128), (96, 16), (256, 128)])
+def test_norm_of_an_infinity(B, d, rot, interleaved, dtype):
+    """1 / sqrt(mean) is 0 there: the infinity's own place is NaN, and its
+    partner's if it is rotated; every other feature is 0."""
+    g = torch.Generator().manual_seed(d + rot)
+    x = torch.randn(6, 3, d, generator=g).to(dtype)
+    for t, (at, v) in enumerate([(0, np.inf), (d - 1, -np.inf), (d // 2 + 3, np.inf),
+                                 (min(rot, d - 1), np.inf), (max(rot - 1, 0), np.inf)]):
+        x[t, 1, at] = v
+    pos = torch.tensor([0, 1, 5, 0, 70000, 2], dtype=torch.int32)
+    f = (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))).float()
+    w = 1 + 0.3 * torch.randn(d, generator=g)
+    got, _ = B.diffattn_qk_norm_rope(x.cuda(), None, pos.cuda(), f.cuda() if rot else None,
+                                     q_weight=w.cuda(), interleaved=interleaved)
+    f64 = f.double().numpy() if rot else None
+    args = (np64(x), np64(w), 1e-6, pos.numpy())
+    with np.errstate(invalid="ignore"):
+        ref = R.norm_rope(*args, f64, interleaved)
+        size = R.pair_size(R.norm_rope(*args, None, interleaved), f64, interleaved)
+    bound = 24 * 2.0 ** -24 * size + (2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -24) * \
+        np.abs(ref)
+    within(got, ref, np.where(np.isnan(bound), 0, bound), "q")
 
 
 # ---- norm: gradients of the weights ------------------------------------------------

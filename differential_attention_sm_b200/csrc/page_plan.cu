@@ -459,6 +459,7 @@ extern "C" int diffattn_page_plan(const int* new_lens, const int* cache_lens, in
   if (n_slots > (1 << 30)) return DA_ERR_UNSUPPORTED;
   const size_t need = diffattn_page_plan_workspace_size(requests, n_slots);
   if (need > 0 && (!workspace || workspace_bytes < need)) return DA_ERR_WORKSPACE;
+  if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % sizeof(int)) return DA_ERR_ALIGNMENT;
   da::PlanArgs a{};
   a.new_lens = new_lens;
   a.lens = cache_lens;

@@ -468,8 +468,8 @@ DA_API size_t diffattn_kv4_page_bytes(int n_kv_heads, int head_dim, int page_siz
  *                   if not served); may be cache_lens
  *   free_count_out: int32 [1], pages left; may be free_count
  * All device pointers.  slots and positions may be NULL with n_slots = 0.
- *   workspace     : device scratch of the queried size (0 for up to 256 slot
- *                   rows; workspace may be NULL then)
+ *   workspace     : device scratch of the queried size, 4-byte aligned (0 for
+ *                   up to 256 slot rows; workspace may be NULL then)
  * Up to 65536 requests and 2^30 slot rows.  DA_ERR_CACHE_FULL goes to
  * dev_status if a request was not served, DA_ERR_PAGE if a token would lie on
  * a page out of range (its slot is -1).  The result depends on the arguments'

@@ -13,6 +13,7 @@ import serving_reference as R
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "differential_attention_sm_b200", "csrc")
+A = 0x10000   # 16-byte aligned fake device address
 NO_TILE, BAD_TILE = 0xFFFFFFFF, 0xFFFFFFFE
 
 
@@ -79,6 +80,14 @@ def test_v1_decode_refuses_an_odd_width(b):
         with pytest.raises(ValueError, match="width"):
             b.diffattn_v1_decode_kv4(q, cache, torch.zeros(5, 2, **i32), torch.zeros(5, **i32),
                                      torch.zeros(4))
+
+
+def test_page_plan_refuses_a_workspace_between_words(b):
+    """Its kernels keep int32 there; a slice of a byte buffer may begin anywhere."""
+    ws = b.diffattn_page_plan_workspace_size(4, 273)
+    for off in (1, 2, 3):
+        args = [A] * 5 + [4, 8, 100, 64, 273] + [A] * 6 + [A + off, ws, None, None]
+        assert b.load().diffattn_page_plan(*args) == b.DA_ERR_ALIGNMENT
 
 
 # ---- the step that the documents show ----------------------------------------------

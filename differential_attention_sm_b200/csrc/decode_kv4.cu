@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) kv4_combine_kernel(const K
   float y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = o[0][i] * r0 - o[1][i] * r1;
-  if (a.apply_norm && n > 0) {
+  if (a.apply_norm && l[0] != 0.f) {  // of 0 it would be a NaN if eps is 0
     float ss = y[0] * y[0] + y[1] * y[1] + y[2] * y[2] + y[3] * y[3];
 #pragma unroll
     for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);

@@ -7,6 +7,7 @@ import torch
 
 import readme_step
 import serving_reference as R
+from parity import status_word
 from test_gpu_serving import check_decode, decode_state, dev, np64, within
 
 pytestmark = pytest.mark.gpu
@@ -34,6 +35,21 @@ def test_window_before_the_first_tile_of_the_cache(B, form, tile):
     table[0, :n_tiles] = [n_tiles - tile + j for j in range(tile)] + list(range(n_tiles - tile))
     assert sorted(table[0, :n_tiles]) == list(range(n_tiles))
     check_decode(B, cache, table, lens, q, [0.4], form, window)
+
+
+# ---- decode: nothing to attend to, and queries that are no numbers ----------------
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_v1_norm_of_a_sequence_without_visible_tokens(B, eps):
+    """All of its pages out of range: 0, also where the norm has no epsilon."""
+    lens = [40, 17, 0]
+    cache, table, q, rng = decode_state(3, lens, 2, 16, 2, seed=31, bad_tail=False)
+    table[1] = [len(cache), -1, 1 << 30]
+    st = status_word()
+    out = B.diffattn_v1_decode_kv4(q.cuda(), dev(cache), dev(table, torch.int32),
+                                   dev(lens, torch.int32), dev([0.4, 0.3], torch.float32),
+                                   apply_norm=True, norm_eps=eps, dev_status=st)
+    assert int(st.item()) == B.DA_ERR_PAGE
+    assert not out[1].any() and not out[2].any() and out[0].any() and torch.isfinite(out).all()
 
 
 # ---- norm: infinities -----------------------------------------------------------------

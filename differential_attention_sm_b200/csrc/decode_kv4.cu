@@ -468,12 +468,15 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) kv4_decode_kernel(const 
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // q * 2^-e is in fp16's range with e the largest exponent of the head.
       // An exponent of 0 or of infinities is replaced: the products are 0 or
-      // not finite either way.
+      // not numbers either way.
       const uint32_t e = min(max(top >> 23, 1u), 253u);
       const float down = __uint_as_float((254u - e) << 23);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         raw[i] = pack_f16(bf16lo(raw[i]) * down, bf16hi(raw[i]) * down);
+      // A head with an infinity has scores that are infinite or NaN, and no
+      // softmax: NaN, where scores of -infinity alone would pass for masked ones.
+      if (top >= 0x7F800000u) raw[0] = 0x7FFF7FFFu;
       // Positive, so that it can multiply a masked score's infinity; scores
       // that this floor touches are 0 to any precision here.
       const float up = fmaxf(__uint_as_float(e << 23) * a.scale, 1.0e-30f);

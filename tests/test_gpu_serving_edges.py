@@ -52,6 +52,39 @@ def test_v1_norm_of_a_sequence_without_visible_tokens(B, eps):
     assert not out[1].any() and not out[2].any() and out[0].any() and torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("form", [1, 2])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_queries_that_are_no_numbers(B, form, value):
+    """Scores of infinities have no softmax: NaN wherever there is a token, also
+    if every score is the lowest; 0 where there is none; other heads as ever."""
+    lens, H = [40, 0, 130], 2
+    cache = torch.zeros(16, H, 16 * 144, dtype=torch.uint8, device="cuda")
+    ones = torch.ones(16 * 16, H, 128, device="cuda")          # every score has q's sign
+    g = torch.Generator().manual_seed(8)
+    v = torch.randn(16 * 16, H, 128, generator=g).cuda()
+    B.diffattn_kv4_append(ones, v, torch.arange(256, dtype=torch.int32, device="cuda"), cache)
+    table = torch.arange(3 * 9, dtype=torch.int32, device="cuda").remainder(16).view(3, 9)
+    q = torch.randn(3, H * form * 2 if form == 2 else H, 128, generator=g).to(torch.bfloat16)
+    ln = dev(lens, torch.int32)
+    run = B.diffattn_v1_decode_kv4 if form == 1 else B.diffattn_v2_decode_kv4
+    lam = torch.rand(H if form == 1 else H * 2, generator=g).cuda()
+    clean = run(q.cuda(), cache, table, ln, lam)
+    for b in range(3):
+        q[b, 1, 70] = value              # V1: branch 2 of head 1; V2: pair 0's second head
+    out = run(q.cuda(), cache, table, ln, lam)
+    hit = 1 if form == 1 else 0
+    for b in (0, 2):
+        assert torch.isnan(out[b, hit]).all()
+    out[:, hit] = clean[:, hit]
+    assert torch.equal(out, clean) and torch.isfinite(clean).all()
+    assert not clean[1].any()
+    if value != value:
+        return
+    only = torch.full_like(q, float(value)).cuda()
+    full = run(only, cache, table, ln, lam)
+    assert torch.isnan(full[0]).all() and torch.isnan(full[2]).all() and not full[1].any()
+
+
 # ---- norm: infinities -----------------------------------------------------------------
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("interleaved", [False, True])

@@ -273,6 +273,10 @@ at::Tensor piece(const at::Tensor& flat, int64_t from, int64_t n) {
   return t;
 }
 
+// The lengths and the count outlive the step; with more slot rows than these they
+// have an allocation of their own (0.4 us), so as not to keep the slot map alive.
+constexpr int64_t kShareRows = 4096;
+
 constexpr const char* kPlanNames[6] = {"slots",  "positions",  "offsets",
                                        "served", "cache_lens", "free_count"};
 
@@ -307,7 +311,8 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   On on(a[10], new_lens, lens, table, pages, n_free, ws, status, out[0], out[1], out[2], out[3],
         out[4], out[5]);
-  // New outputs, and the scratch if none was brought, are pieces of one allocation.
+  // New outputs, and the scratch if none was brought, are pieces of one allocation
+  // (or two).
   void* scratch = ws ? ws->data_ptr() : nullptr;
   size_t scratch_bytes = ws ? ws->nbytes() : 0;
   if (ws && !ws->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
@@ -316,9 +321,13 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (fresh) {
     const int64_t pieces = 2 * (int64_t)n_slots + 3 * R + 2;
     own = at::empty({pieces + (int64_t)(scratch_need + 3) / 4}, new_lens.options());
+    const bool apart = n_slots > kShareRows;
+    at::Tensor kept;
+    if (apart) kept = at::empty({R + 1}, new_lens.options());
     int64_t from = 0;
     for (int i = 0; i < 6; ++i) {
-      out[i] = piece(own, from, sizes[i]);
+      if (i == 4 && apart) from = 0;
+      out[i] = piece(i >= 4 && apart ? kept : own, from, sizes[i]);
       from += sizes[i];
     }
     scratch = scratch_need ? address<int>(own) + pieces : scratch;

@@ -20,6 +20,23 @@ def B():
     return binding
 
 
+# ---- page plan: what a server keeps --------------------------------------------------
+def test_kept_lengths_do_not_hold_the_slot_map(B):
+    """The lengths and the count that the next step takes lie apart from a large
+    step's slot map."""
+    R_, n = 5, 50000
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, stack = torch.full((R_, 800), -1, **i32), torch.arange(4000, **i32)
+    args = (torch.full((R_,), 9000, **i32), torch.zeros(R_, **i32), table, stack,
+            torch.full((1,), 4000, **i32), 16, n)
+    plan = B.diffattn_page_plan(*args)
+    for name in ("cache_lens", "free_count"):
+        assert plan[name].untyped_storage().nbytes() <= 4 * (R_ + 1)
+    ref = R.page_plan([9000] * R_, [0] * R_, np.full((R_, 800), -1), np.arange(4000), 4000, 16, n)
+    for name in plan:
+        assert np.array_equal(plan[name].cpu().numpy(), ref[name]), name
+
+
 # ---- decode: windows that begin inside a stage ---------------------------------
 @pytest.mark.parametrize("form", [1, 2])
 @pytest.mark.parametrize("tile", [0, 1, 2, 3, 5, 7, 9, 33])

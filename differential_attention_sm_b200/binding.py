@@ -667,6 +667,9 @@ def _serving():
         except ImportError as e:
             raise ImportError("_marshal.so not built (run __graft_entry__.build() or "
                               "python -m differential_attention_sm_b200.build)") from e
+        if m.torch_version != torch.__version__:   # it builds tensors by torch's C++ interface
+            raise ImportError("_marshal.so was built for torch %s, not %s (run "
+                              "__graft_entry__.build())" % (m.torch_version, torch.__version__))
         m.bind(lib._handle, DiffAttnError)
         _marshal = m
     return _marshal

@@ -97,6 +97,7 @@ def build_marshal(force: bool = False) -> str:
     tmp = MARSHAL + ".%d.tmp" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared",
            "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           '-DDA_TORCH_VERSION="%s"' % torch.__version__,
            "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE,
            "-I" + os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
            "-isystem", os.path.join(root, "include"),

@@ -22,6 +22,11 @@
 
 #include "diffattn.h"
 
+// The torch whose headers this was compiled against (build.py passes it).
+#ifndef DA_TORCH_VERSION
+#error "DA_TORCH_VERSION is not defined"
+#endif
+
 namespace {
 
 #define DA_CALLS(X)                           \
@@ -678,4 +683,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", DA_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -90,6 +90,16 @@ def test_page_plan_refuses_a_workspace_between_words(b):
         assert b.load().diffattn_page_plan(*args) == b.DA_ERR_ALIGNMENT
 
 
+def test_marshalling_module_of_another_torch_is_refused(b, monkeypatch):
+    """It is compiled against one torch's C++ interface."""
+    monkeypatch.setattr(b, "_marshal", None)
+    with monkeypatch.context() as other:
+        other.setattr(torch, "__version__", "0.0.0")
+        with pytest.raises(ImportError, match="0.0.0"):
+            b._serving()
+    assert b._marshal is None and b._serving().torch_version == torch.__version__
+
+
 # ---- the step that the documents show ----------------------------------------------
 class Definitions:
     """The calls of a serving step by their definitions, on the CPU."""

@@ -7,6 +7,7 @@ import torch
 
 import readme_step
 import serving_reference as R
+import test_gpu_serving as S
 from parity import status_word
 from test_gpu_serving import check_decode, decode_state, dev, np64, within
 
@@ -153,3 +154,136 @@ def test_weight_gradient_of_many_rows(B):
 # ---- the step that the documents show ----------------------------------------------
 def test_readme_step_keeps_the_page_pool(B):
     readme_step.run(B, "cuda")
+
+
+# ---- main loops: more work than the grid has places ---------------------------------
+def long_state(lens, Hkv, page, cols, seed, pages=24):
+    """A few distinct pages, used over and over; scores that rise and fall from
+    page to page by more than the running maximum's slack."""
+    rng = np.random.default_rng(seed)
+    cache = rng.integers(0, 256, (pages, Hkv, page * 144)).astype(np.uint8)
+    tiles = cache.reshape(pages, Hkv, -1, 2304)
+    tiles[..., 2048:] = rng.integers(13 * 8, 15 * 8, tiles[..., 2048:].shape)
+    tiles[..., 2048:2176] += (8 * (np.arange(pages) % 4)).astype(np.uint8)[:, None, None, None]
+    per = max(1, -(-max(lens) // page))
+    table = rng.integers(0, pages, (len(lens), per))
+    table[::3] = (table[::3, :1] + np.arange(per)) % pages     # neighbours in memory, too
+    for b, n in enumerate(lens):
+        table[b, -(-n // page):] = -1
+    q = torch.tensor(rng.standard_normal((len(lens), cols, 128)), dtype=torch.bfloat16)
+    rows = [np.stack(R.cache_rows(cache, np.arange(pages)[:, None], [page] * pages, kind))
+            for kind in "kv"]                                  # [pages][heads, page, 128]
+    return cache, table, q, rng, rows
+
+
+@pytest.mark.parametrize("form,Bn,longest,Hkv,group,page,window", [
+    (2, 200, 3600, 3, 2, 64, 0),            # one column tile; segments found by sums
+    (2, 330, 3000, 2, 8, 16, 0),            # segments written down
+    (2, 1, 72001, 16, 2, 32, 0),            # one sequence over all warps
+    (2, 400, 4100, 2, 4, 16, 1500),
+    (2, 340, 4300, 1, 10, 32, 0),           # two column tiles
+    (2, 1, 45000, 16, 12, 64, 0),
+    (1, 150, 3600, 5, 1, 64, 0),
+    (1, 300, 3000, 3, 1, 16, 2200),
+])
+def test_decode_of_many_stages(B, form, Bn, longest, Hkv, group, page, window):
+    """Runs of 10 stages and more, which pass from head to head and from sequence
+    to sequence: each warp's ring goes round, its tile indices are looked up anew,
+    and its maximum and sums are carried from stage to stage."""
+    rng = np.random.default_rng(Bn + Hkv)
+    lens = [longest] if Bn == 1 else list(rng.integers(longest // 2, longest, Bn))
+    if Bn > 1:
+        lens[5], lens[6], lens[90] = 0, 1, 64
+    lens = [int(n) for n in lens]
+    cache, table, q, rng, (Kp, Vp) = long_state(lens, Hkv, page, Hkv * group, seed=Bn + page)
+    chunks = -(-group // 16)
+    seen = [(max(0, n - window) if window else 0, n) for n in lens]
+    stages = sum((n - 1) // 64 - lo // 64 + 1 for lo, n in seen if n) * Hkv * chunks
+    warps = 148 * (12 if group <= 8 else 8)
+    assert stages > 9 * warps, stages
+    lam = rng.uniform(-0.5, 1.2, Hkv if form == 1 else Hkv * group // 2)
+    st = status_word()
+    run = B.diffattn_v1_decode_kv4 if form == 1 else B.diffattn_v2_decode_kv4
+    args = (q.cuda(), dev(cache), dev(table, torch.int32), dev(lens, torch.int32),
+            dev(lam, torch.float32))
+    out = run(*args, window=window, dev_status=st)
+    assert int(st.item()) == 0
+    assert torch.equal(out, run(*args, window=window))
+    lam64 = np.asarray(lam, np.float32).astype(np.float64)
+    some = range(Bn) if Bn == 1 else sorted({5, 6, 90, *rng.permutation(Bn)[:60].tolist()})
+    heads = group // 2 if form == 2 else 1          # outputs of a KV head
+    q64 = np64(q)
+    for b in some:
+        n = lens[b]
+        for h in range(Hkv):
+            at = table[b, :-(-n // page)]
+            K, V = (x[at, h].reshape(-1, 128)[None, :n] for x in (Kp, Vp))
+            sl = slice(h * heads, (h + 1) * heads)
+            ref, bound = R.decode(q64[b, h * group:(h + 1) * group], K, V, lam64[sl], form, window)
+            within(out[b, sl], ref, bound + 2.0 ** -8 * np.abs(ref), "sequence %d head %d" % (b, h))
+
+
+@pytest.mark.parametrize("case", [
+    # T, Hq, Hk, d, rot, interleaved, dtype, fused, weights, far
+    (3000, 32, 8, 128, 128, False, torch.bfloat16, True, True, 1 << 20),
+    (3000, 32, 8, 128, 64, True, torch.float32, False, True, 9000),
+    (9001, 5, 2, 64, 64, True, torch.bfloat16, True, True, 9000),
+    (6000, 3, 1, 256, 128, False, torch.float32, True, False, 9000),
+    (20000, 2, 0, 32, 32, False, torch.float32, False, True, 30000),
+])
+def test_norm_of_many_batches(B, case):
+    """CTAs that take several batches of tokens: both angle buffers, and rows on
+    their way from one batch into the next; forward and backward."""
+    S.test_norm_rope(B, *case)
+    S.test_norm_rope_bwd(B, *case)
+
+
+@pytest.mark.parametrize("T,H,page,dtype", [
+    (8000, 16, 64, torch.bfloat16),
+    (8000, 16, 16, torch.float32),
+    (30000, 3, 32, torch.bfloat16),
+    (30000, 7, 128, torch.float32),
+])
+def test_append_and_read_of_many_rows(B, T, H, page, dtype):
+    """CTAs that walk over the heads: the next row on its way while one is packed,
+    and several heads' codes asked for at once; byte by byte."""
+    rng = np.random.default_rng(T + H)
+    base = S.rows_for_cache(rng, 300, 1, dtype)[:, 0]             # rows, used over and over
+    idx = [rng.integers(0, 300, (T, H)) for _ in "kv"]
+    kd, vd = (base[torch.as_tensor(i)].cuda() for i in idx)
+    pages = T // page + 3
+    slots = rng.permutation(pages * page)[:T]
+    slots[rng.random(T) < 0.05] = -1
+    before = rng.integers(0, 256, (pages, H, page * 144)).astype(np.uint8)
+    cache, st = dev(before), status_word()
+    B.diffattn_kv4_append(kd, vd, dev(slots, torch.int32), cache, dev_status=st)
+    assert int(st.item()) == 0
+    want = before.copy()
+    sb, codes = R.quantise(np64(base))
+    live = np.flatnonzero(slots >= 0)
+    p, u = slots[live] // page, slots[live] % page
+    head = np.arange(H)[None, :, None]
+    for kind, i in zip("kv", idx):
+        at, at_s = R.byte_of(kind, np.arange(16)[:, None], np.arange(0, 128, 2)[None])
+        where = (u // 16 * 2304)[:, None] + at[u % 16]
+        pair = codes[:, 0::2] | (codes[:, 1::2] << 4)
+        want[p[:, None, None], head, where[:, None]] = pair[i[live]]
+        _, at_s = R.byte_of(kind, np.arange(16)[:, None], np.arange(0, 128, 16)[None])
+        where = (u // 16 * 2304)[:, None] + at_s[u % 16]
+        want[p[:, None, None], head, where[:, None]] = sb[i[live]]
+    got = cache.cpu().numpy()
+    # a negative value that rounds to 0 may be held as -0: code 8 stands for 0 too
+    is_code = np.tile(np.arange(2304) < 2048, page // 16)
+    for x in (got, want):
+        c = x[..., is_code]
+        c = np.where(c & 15 == 8, c & 0xF0, c)
+        x[..., is_code] = np.where(c >> 4 == 8, c & 0x0F, c)
+    assert np.array_equal(got, want)
+    held = R.held(np64(base))
+    for out_dtype in (torch.bfloat16, torch.float32):
+        out = tuple(torch.full((T, H, 128), 7.0, dtype=out_dtype, device="cuda") for _ in "kv")
+        B.diffattn_kv4_read(cache, dev(slots, torch.int32), out=out)
+        for i, o in zip(idx, out):
+            ref = held[i]
+            ref[slots < 0] = 7.0
+            assert np.array_equal(np64(o), ref, equal_nan=True)

@@ -287,3 +287,109 @@ def test_append_and_read_of_many_rows(B, T, H, page, dtype):
             ref = held[i]
             ref[slots < 0] = 7.0
             assert np.array_equal(np64(o), ref, equal_nan=True)
+
+
+# ---- calls that are allowed and rare -------------------------------------------------
+def test_step_captured_over_two_streams(B):
+    """A step whose norm runs beside the plan and joins it before the append: each
+    call's launches wait for both of what they come after."""
+    Rn, H, page, n_pages, T = 300, 2, 16, 700, 900
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(T, 8, 128, generator=g).to(torch.bfloat16).cuda()
+    pos = torch.arange(T, **i32)
+    f = torch.rand(64, generator=g).cuda()
+    lam = torch.tensor([0.2, 0.7], device="cuda")
+    ws = torch.empty(B.diffattn_v2_decode_kv4_workspace_size(Rn, 4, H), dtype=torch.uint8,
+                     device="cuda")
+    table, stack = torch.full((Rn, 4), -1, **i32), torch.arange(n_pages, **i32)
+    new = torch.tensor([1 + i % 5 for i in range(Rn)], **i32)
+    lens, count = torch.zeros(Rn, **i32), torch.full((1,), n_pages, **i32)
+    cache = torch.zeros(n_pages, H, page * 144, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(other):
+        main = torch.cuda.current_stream()
+        if other is not None:
+            other.wait_stream(main)
+        q, k = B.diffattn_qk_norm_rope(x[:, :4], x[:, 4:6], pos, f, stream=other)
+        p = B.diffattn_page_plan(new, lens, table, stack, count, page, T)
+        if other is not None:
+            main.wait_stream(other)
+        B.diffattn_kv4_append(k, x[:, 6:], p["slots"], cache)
+        last = (p["offsets"][1:] - 1).long()
+        return p, B.diffattn_v2_decode_kv4(q[last], cache, table, p["cache_lens"], lam,
+                                           workspace=ws)
+
+    p, want = step(None)
+    want, slots = want.clone(), p["slots"].clone()
+    assert bool(p["served"].all()) and torch.isfinite(want).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p, out = step(side)
+    for _ in range(5):
+        cache.zero_()
+        table.fill_(-1)
+        for t in (out, p["slots"], p["cache_lens"]):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(p["slots"], slots)
+
+
+def test_norm_of_a_token_of_very_many_heads(B):
+    S.test_norm_rope(B, 1, 100000, 3, 16, 16, False, torch.bfloat16, False, True, 70)
+    # the weights' gradient by terms of one sign: 22 half steps of a term, 128 adds
+    # in fp32 and 6 behind them
+    g = torch.Generator().manual_seed(1)
+    x = torch.rand(1, 100000, 16, generator=g) + 0.5
+    dy = torch.rand(1, 100000, 16, generator=g) + 0.5
+    w = torch.ones(16)
+    got = B.diffattn_qk_norm_rope_bwd(x.cuda(), None, dy.cuda(), None, None, None,
+                                      q_weight=w.cuda())
+    dx, dw = R.norm_rope_bwd(np64(x), np64(w), 1e-6, np.zeros(1), None, False, np64(dy))
+    within(got["dq_weight"], dw, (22 + 128 + 6) * 2.0 ** -24 * np.abs(dw), "dq_weight")
+
+
+def test_positions_before_the_first(B):
+    """Angles of negative positions turn the other way, to the far end of int32."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(4, 2, 64, generator=g)
+    pos = torch.tensor([-1, -2 ** 31, 2 ** 31 - 1, -4097], dtype=torch.int32)
+    f = (10000.0 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64)).float()
+    got, _ = B.diffattn_qk_norm_rope(x.cuda(), None, pos.cuda(), f.cuda())
+    args = (np64(x), np.ones(64), 1e-6, pos.numpy())
+    f64 = f.double().numpy()
+    size = R.pair_size(R.norm_rope(*args, None, False), f64, False)
+    within(got, R.norm_rope(*args, f64, False), 25 * 2.0 ** -24 * size, "q")
+
+
+def test_release_and_plan_take_turns_in_a_graph(B):
+    """A captured release and plan, replayed: the pages go round and none is lost."""
+    Rn, page, n_pages = 40, 16, 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, stack = torch.full((Rn, 4), -1, **i32), torch.arange(n_pages, **i32)
+    lens, count = torch.zeros(Rn, **i32), torch.full((1,), n_pages, **i32)
+    gone, new = torch.zeros(Rn, **i32), torch.zeros(Rn, **i32)
+    out = dict(slots=torch.empty(600, **i32), positions=torch.empty(600, **i32),
+               offsets=torch.empty(Rn + 1, **i32), served=torch.empty(Rn, **i32),
+               cache_lens=lens, free_count=count)
+    ws = torch.empty(B.diffattn_page_plan_workspace_size(Rn, 600), dtype=torch.uint8,
+                     device="cuda")
+
+    def step():
+        B.diffattn_page_release(gone, lens, table, stack, count, page)
+        B.diffattn_page_plan(new, lens, table, stack, count, page, 600, out=out, workspace=ws)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rng = np.random.default_rng(1)
+    for _ in range(12):
+        gone.copy_(torch.as_tensor((rng.random(Rn) < 0.3).astype(np.int32)))
+        new.copy_(torch.as_tensor(rng.integers(0, 20, Rn).astype(np.int32)))
+        graph.replay()
+        held = [int(t) for row, n in zip(table.tolist(), lens.tolist())
+                for t in row[:-(-n // page)]]
+        assert sorted(held + stack.tolist()[:int(count)]) == list(range(n_pages))

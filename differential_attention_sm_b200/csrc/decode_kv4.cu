@@ -22,17 +22,19 @@
 //    never pass through shared memory again.  (tcgen05 would want them
 //    written back to shared or tensor memory first, and 16 columns at least;
 //    its rate is not what is missing here.)
-//  - q is scaled by a power of two per head into fp16's range (exact), p is
-//    rounded to fp16 (half a step is 2^-11 of a probability; the sums l and O
-//    are fp32).  m moves only when a score passes it by more than 2^10, so p
-//    reaches 2^15 at most and the common stage needs no maximum across lanes.
+//  - q is scaled by a power of two per head into fp16's range: exact down to
+//    2^-17 of the head's largest feature; what is smaller is rounded, by 2^-25
+//    of the largest at most.  p is rounded to fp16 (half a step is 2^-11 of a
+//    probability), the sums l (of the unrounded p) and O are fp32.  m moves only
+//    when a score passes it by more than 2^10, so p reaches 2^15 at most and the
+//    common stage needs no maximum across lanes.
 // A run leaves (O, l, m) of each sequence and head that it touches in the
 // workspace; a second kernel joins them, subtracts, and normalises.
 //
 // Measured, 64 sequences of 32768 entries, 8 KV heads, 64 query heads (2.4 GB):
-// 377 us in bursts at 1965 MHz, 0.98 of the copy rate (the copies alone 363);
-// 430 to 460 us when the board's power limit sets the clock.  V1, 16 x 8191 x
-// 32 heads (0.6 GB): 100 to 117 us.
+// 377 to 387 us in bursts at 1965 MHz, 0.95 to 0.98 of the copy rate (the copies
+// alone 363); 450 to 475 us when the board's power limit sets the clock (1550 MHz
+// at 995 W).  V1, 16 x 8191 x 32 heads (0.6 GB): 108 to 120 us.
 // A tile and head costs 238 instructions: 64 conversions, 64 multiplications
 // and 16 matrix instructions, which hold the former two up for 7 of their 8
 // clocks, make 285 of about 400 clocks of an SM quarter, where the memory

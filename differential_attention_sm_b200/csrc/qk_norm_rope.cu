@@ -21,8 +21,8 @@
 // their way through shared memory several turns ahead: registers alone held
 // too few bytes in flight (72 us where this takes 58).  This file is built
 // without fast math: with fp32 rows the outputs are compared at fp32's own steps.
-// Measured: 16384 tokens of 40 heads of 128 58 us, 0.88 of the copy rate; the
-// backward, 64 heads of 64, 109 us, 0.94.
+// Measured: 16384 tokens of 40 heads of 128 58 to 60 us, 0.85 to 0.88 of the copy
+// rate; the backward, 64 heads of 64, 116 to 118 us, 0.87.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -99,7 +99,8 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], cons
 }
 
 // cos and sin of the batch's tokens.  The product of a 32-bit position and an
-// fp32 frequency is formed in 64 bits and reduced to a part of one turn there.
+// fp32 frequency is formed in 64 bits and reduced to a part of one turn there;
+// rounding that part to fp32 moves the angle by pi * 2^-25 at most.
 __device__ __forceinline__ void angles(const NormArgs& a, int tok0, float* cs, float* sn) {
   const int half = a.rot >> 1, n = half << a.tok_log2;
   for (int i = threadIdx.x; i < n; i += kThreads) {

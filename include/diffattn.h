@@ -556,7 +556,8 @@ DA_API int diffattn_v1_decode_kv4(const void* q, const void* cache, int n_pages,
  *   q_weight, k_weight: device fp32 [head_dim], 16-byte aligned, or NULL (ones)
  *   positions   : device int32 [tokens]; inv_freq: device fp32 [rot_dim / 2];
  *                 both may be NULL with rot_dim = 0 (norm only)
- * Angles are formed in 64 bits.  head_dim and rot_dim multiples of 16,
+ * Angles are formed in 64 bits, a row's sum of squares in fp32: rows whose sum
+ * passes its range (features of 1e19) give 0.  head_dim and rot_dim multiples of 16,
  * head_dim <= 256, at most 2^30 tokens and 2^20 heads of each kind
  * (DA_ERR_UNSUPPORTED otherwise). */
 DA_API int diffattn_qk_norm_rope(const void* q, long long q_token_stride, const void* k,

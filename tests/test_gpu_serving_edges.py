@@ -393,3 +393,42 @@ def test_release_and_plan_take_turns_in_a_graph(B):
         held = [int(t) for row, n in zip(table.tolist(), lens.tolist())
                 for t in row[:-(-n // page)]]
         assert sorted(held + stack.tolist()[:int(count)]) == list(range(n_pages))
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,rot,interleaved,dtype", [
+    (700, 5, 3, 16, 16, False, torch.bfloat16),      # several rows of a line of memory
+    (3000, 32, 8, 128, 128, True, torch.bfloat16),
+    (41, 3, 2, 48, 16, False, torch.float32),
+])
+def test_norm_in_place_on_a_fused_projection(B, T, Hq, Hk, d, rot, interleaved, dtype):
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, (Hq + 2 * Hk) * d, generator=g).to(dtype).cuda()
+    before = x.clone()
+    q, k, v = (t.unflatten(1, (-1, d)) for t in x.split([Hq * d, Hk * d, Hk * d], 1))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    f = torch.rand(rot // 2, generator=g).cuda()
+    w = torch.rand(d, generator=g).cuda()
+    kw = dict(q_weight=w, interleaved=interleaved)
+    want = B.diffattn_qk_norm_rope(q, k, pos, f, **kw)
+    assert torch.equal(x, before)
+    B.diffattn_qk_norm_rope(q, k, pos, f, **kw, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert torch.equal(x[:, (Hq + Hk) * d:], before[:, (Hq + Hk) * d:])
+
+
+def test_streams_by_number_and_by_object(B):
+    """The default stream is number 0."""
+    x = torch.randn(64, 3, 128, device="cuda")
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    f = torch.rand(64, device="cuda")
+    want = B.diffattn_qk_norm_rope(x, None, pos, f)[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (0, torch.cuda.default_stream(), side, side.cuda_stream, None):
+        got = B.diffattn_qk_norm_rope(x, None, pos, f, stream=s)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    with torch.cuda.stream(side):
+        got = B.diffattn_qk_norm_rope(x, None, pos, f)[0]
+        side.synchronize()
+        assert torch.equal(got, want) and torch.cuda.current_stream() == side

@@ -432,3 +432,49 @@ def test_streams_by_number_and_by_object(B):
         got = B.diffattn_qk_norm_rope(x, None, pos, f)[0]
         side.synchronize()
         assert torch.equal(got, want) and torch.cuda.current_stream() == side
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,rot,interleaved,dtype", [
+    (12000, 96, 30, 128, 64, True, torch.bfloat16),
+    (20000, 100, 30, 64, 64, False, torch.float32),
+    (25001, 90, 31, 48, 16, False, torch.bfloat16),        # idle lanes
+    (9000, 40, 31, 256, 256, False, torch.float32),
+])
+def test_norm_gradients_of_very_many_rows(B, T, Hq, Hk, d, rot, interleaved, dtype):
+    """More rows of a thread than it adds up in fp32 (queries, keys, both layouts),
+    against the formulas in 64 bits."""
+    lanes = 1 << (max(d - 1, 0) // 16).bit_length()
+    assert T * (Hq + Hk) > 128 * 296 * (256 // lanes)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    pos = torch.randint(0, 9000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    f = (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float().cuda()
+    x = [rnd(T, H, d).to(dtype) for H in (Hq, Hk)]
+    dy = [rnd(T, H, d) for H in (Hq, Hk)]
+    w = [1 + 0.3 * rnd(d) for _ in "qk"]
+    eps = 1e-3
+    args = (*x, *dy, pos, f)
+    kw = dict(q_weight=w[0], k_weight=w[1], norm_eps=eps, interleaved=interleaved)
+    out = B.diffattn_qk_norm_rope_bwd(*args, **kw)
+    again = B.diffattn_qk_norm_rope_bwd(*args, **kw)
+    for name in out:
+        assert torch.equal(out[name], again[name]), name
+    ang = pos.double()[:, None] * f.double()
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+    i = torch.arange(rot // 2, device="cuda")
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    u = 2.0 ** -24
+    for xx, yy, ww, name in zip(x, dy, w, "qk"):
+        xx, yy, ww = xx.double(), yy.double(), ww.double()
+        t, gs = yy.clone(), yy.abs()
+        t[..., a] = yy[..., a] * c + yy[..., b] * s
+        t[..., b] = yy[..., b] * c - yy[..., a] * s
+        gs[..., a] = gs[..., b] = yy[..., a].abs() + yy[..., b].abs()
+        r = 1 / (xx.square().mean(-1, keepdim=True) + eps).sqrt()
+        n, wg = xx * r, ww * t
+        dx = r * (wg - n * (n * wg).mean(-1, keepdim=True))
+        size = r * (ww.abs() * gs + n.abs() * (n.abs() * ww.abs() * gs).mean(-1, keepdim=True))
+        assert bool(((out["d" + name].double() - dx).abs() <= 64 * u * size).all()), name
+        dw, terms = (t * n).sum((0, 1)), (gs * n.abs()).sum((0, 1))
+        off = (out["d%s_weight" % name].double() - dw).abs()
+        assert bool((off <= (22 + 128 + 6) * u * terms).all()), name
